@@ -406,6 +406,117 @@ size_t kvq_decode_noalloc_scratch_bytes(void);
  * was 0, else the recorded kvq_status (e.g. KVQ_ERR_TIMEOUT). */
 kvq_status kvq_decode_noalloc_status(void* stream, int* device_code);
 
+/* ---------------------------------------------------------------- rotary positions */
+
+/* Rotary positions with one or several axes (text: one; images and video: time, height,
+ * width). Block b (dims b and b + 64) of token i turns by the angle of position
+ * positions[axis[b] * axis_stride + i]. The angles' cosines and sines come from the caller's
+ * table, so any base, scaling or interpolation is the caller's choice; build it in 64 bits
+ * (fp32 angles of far positions are off by more than a rotation's worth of digits).
+ * A position outside 0..n_positions-1 is never looked up: see kvq_rope and kvq_paged_append. */
+typedef struct {
+  const float* table;        /* [n_positions][64][2]: cos, sin; 16-byte aligned */
+  const int32_t* positions;  /* [n_axes][tokens], axis a at a * axis_stride */
+  int64_t axis_stride;
+  int32_t n_positions;
+  int32_t n_axes;            /* 1..4 */
+  uint8_t axis[64];          /* axis of block b, < n_axes */
+} kvq_rope_desc;
+
+/* out = x rotated: with (c, s) of block b, out_b = fl(fl(x_b c) - fl(x_b+64 s)) and
+ * out_b+64 = fl(fl(x_b+64 c) + fl(x_b s)) in fp32, rounded once to x's type.
+ * x, out: [batch][n_heads][seq_len][128], same shape and dtype, strides as they come; token
+ * (b, t) has the position index b * seq_len + t. out may be x itself, and may not overlap it
+ * in any other way. Blocks whose position is outside the table come out as NaN. */
+kvq_status kvq_rope(const void* x, const kvq_tensor4* xd, const kvq_rope_desc* rope, void* out,
+                    const kvq_tensor4* od, void* stream);
+
+/* ---------------------------------------------------------------- paged packed cache */
+
+/* Shape of a pool of pages (one layer), each holding page_tokens positions of one sequence
+ * for every KV head. */
+typedef struct {
+  int32_t n_pages;
+  int32_t page_tokens;       /* a multiple of 32, at most 65536 */
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t bits_k;
+  int32_t bits_v;            /* 1..8: a pool always holds its values */
+} kvq_paged_desc;
+
+/* The pages of a batch of sequences. Position p of sequence b is in page
+ * block_table[b * table_stride + p / page_tokens]. All arrays are device memory, so one
+ * captured graph serves changing batches; batch is 1..1024. */
+typedef struct {
+  const int32_t* block_table;
+  const int32_t* seq_lens;   /* [batch] positions stored (append: before the call) */
+  int64_t table_stride;
+  int32_t batch;
+  int32_t max_pages;         /* entries of a table row that may be read */
+} kvq_page_table;
+
+/* Bytes of a pool: a header of kvq_packed_header_bytes(n_kv_heads) bytes, then n_pages pages
+ * of n_kv_heads * page_tokens / 32 tile records (kvq_quantize's records, head-major inside the
+ * page). Returns 0 for an invalid descriptor. */
+size_t kvq_paged_bytes(const kvq_paged_desc* desc);
+
+/* Writes the pool's header (kvq_packed_header with magic "KVQP", n_pages as `batch`,
+ * page_tokens as `capacity`, status 0, and the allocation's digests); the pages are left as
+ * they are. Call it once before the first append, or again to clear a status.
+ * alloc: records from kvq_calibrate with bits_k == desc->bits_k. pool: kvq_paged_bytes(desc)
+ * bytes, 16-byte aligned. */
+kvq_status kvq_paged_init(const void* alloc, const kvq_paged_desc* desc, void* pool, void* stream);
+
+/* Appends new tokens of a ragged batch to their pages, rotated on the way: rows
+ * cu_tokens[b] .. cu_tokens[b + 1] - 1 of K and V become positions seq_lens[b] .. of sequence
+ * b. Keys are rotated as by kvq_rope (rounded to their dtype, as a model would have cached
+ * them) unless rope is NULL; then keys and values are quantized exactly as by kvq_quantize, so
+ * any split of a sequence over calls stores the same bytes. Token i of the call (row i) has
+ * position index i. Tokens already in a partly filled tile are kept; the rest of the last
+ * tile is stored as code 0, norm 0; no other byte is touched. Rows from cu_tokens[batch] on
+ * are not read. A sequence may get no token.
+ * K, V: [1][n_kv_heads][n_tokens][128] (one dtype; strides may differ).
+ * The pages written must belong to one sequence each. cu_tokens: [batch + 1], device memory.
+ * The call checks the pool's header on the device (KVQ_ERR_MISMATCH, nothing written) and every page
+ * index, length and position it uses: a sequence whose rows or positions do not fit (rows not ascending
+ * or past n_tokens, more positions than max_pages hold, a page outside the pool) loses the tiles
+ * concerned, a token whose position is outside the table is stored with a NaN norm, and the
+ * header's status becomes KVQ_ERR_RANGE (kvq_packed_status), which stays until kvq_paged_init:
+ * later appends still write what fits, later decodes report it. n_tokens is at least 1. */
+kvq_status kvq_paged_append(const void* K, const kvq_tensor4* kd, const void* V, const kvq_tensor4* vd,
+                            const kvq_rope_desc* rope, const void* alloc, const kvq_paged_desc* desc,
+                            const kvq_page_table* seqs, const int32_t* cu_tokens, void* pool, void* stream);
+
+/* A prefix that every sequence of a batch attends to before its own positions: `seq_len`
+ * positions in the listed pages of the same pool (the last page may be partly used). */
+typedef struct {
+  const int32_t* pages;      /* [n_pages], device memory */
+  int32_t n_pages;           /* >= ceil(seq_len / page_tokens) */
+  int32_t seq_len;
+} kvq_prefix;
+
+/* Workspace bytes kvq_paged_decode_attn needs for this batch size and query head count, with
+ * a prefix (prefix_len > 0, any length) or without one. */
+size_t kvq_paged_decode_workspace_bytes(const kvq_paged_desc* desc, int batch, int n_q_heads, int prefix_len);
+
+/* Decode attention over a paged cache, one query token per sequence: query head hq of sequence
+ * b attends with KV head hq / (n_q_heads / n_kv_heads) over the prefix (if any) and then the
+ * sequence's own positions 0..seq_lens[b]-1, in one softmax; arithmetic and dequantization
+ * as kvq_decode_attn. The prefix is dequantized once for the whole batch, not once per
+ * sequence. A sequence with nothing to attend to gives a row of zeros.
+ * q: [batch][n_q_heads][1][128], rotated (kvq_rope); n_q_heads / n_kv_heads must be 1..8.
+ * out: [batch][n_q_heads][128], contiguous, 16-byte aligned, of out_dtype (any kvq_dtype,
+ * rounded once from fp32).
+ * prefix: NULL or seq_len 0 for none.
+ * ws: kvq_paged_decode_workspace_bytes bytes, zeroed once by kvq_workspace_init; calls that
+ * share it must not overlap. Its status word reports (kvq_workspace_status) a header mismatch
+ * or a status left in the pool, KVQ_ERR_RANGE for a length above max_pages * page_tokens or
+ * below 0 or a page outside the pool, and KVQ_ERR_TIMEOUT; rows of `out` that such an error
+ * concerns are left as they are. */
+kvq_status kvq_paged_decode_attn(const void* q, const kvq_tensor4* qd, const void* pool, const void* alloc,
+                                 const kvq_paged_desc* desc, const kvq_page_table* seqs, const kvq_prefix* prefix,
+                                 void* out, int out_dtype, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,7 +13,10 @@
 #include "common.cuh"
 #include "decode.cuh"
 #include "nf4.cuh"
+#include "paged.cuh"
+#include "prefix.cuh"
 #include "quantize.cuh"
+#include "rope.cuh"
 
 using namespace kvq;
 
@@ -908,6 +911,413 @@ kvq_status kvq_decode_noalloc_status(void* stream, int* device_code) {
   }
   if (device_code) *device_code = static_cast<int>(code);
   return code == 0 ? KVQ_OK : static_cast<kvq_status>(code);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------------------------
+// Rotary positions and the paged packed cache.
+namespace {
+
+// Rotation arguments of a description over `n_tokens` tokens.
+kvq_status rope_args(const kvq_rope_desc* r, int64_t n_tokens, RopeArgs* out) {
+  if (!r->table || !r->positions || !aligned16(r->table)) return KVQ_ERR_ARG;
+  if (r->n_positions < 1 || r->n_axes < 1 || r->n_axes > 4) return KVQ_ERR_SHAPE;
+  if (r->n_axes > 1 && r->axis_stride < n_tokens) return KVQ_ERR_ARG;
+  for (int b = 0; b < kH; ++b)
+    if (r->axis[b] >= r->n_axes) return KVQ_ERR_ARG;
+  out->table = reinterpret_cast<const float2*>(r->table);
+  out->positions = r->positions;
+  out->axis_stride = r->n_axes > 1 ? r->axis_stride : 0;
+  out->n_positions = r->n_positions;
+  out->n_axes = r->n_axes;
+  std::memcpy(out->axis, r->axis, sizeof(out->axis));
+  return KVQ_OK;
+}
+
+// True if no two rows of a view share bytes (it may be written).
+bool rows_apart(const kvq_tensor4* t) {
+  std::pair<int64_t, int64_t> d[3] = {{t->stride_b, t->batch}, {t->stride_h, t->n_heads}, {t->stride_t, t->seq_len}};
+  std::sort(d, d + 3);
+  int64_t extent = kD;                       // elements up to the end of the last row so far
+  for (const auto& x : d) {
+    if (x.second == 1) continue;
+    if (x.first < extent) return false;
+    extent += x.first * (x.second - 1);
+  }
+  return true;
+}
+
+bool paged_ok(const kvq_paged_desc* d) {
+  return d && d->n_pages >= 1 && d->page_tokens >= kTile && d->page_tokens % kTile == 0 && d->page_tokens <= 65536 &&
+         d->n_kv_heads >= 1 && d->head_dim == kD && d->bits_k >= 1 && d->bits_k <= 8 && d->bits_v >= 1 && d->bits_v <= 8;
+}
+
+kvq_status paged_args(const kvq_paged_desc* d, const kvq_page_table* s, PagedArgs* out) {
+  if (!paged_ok(d)) return KVQ_ERR_ARG;
+  PagedArgs a{};
+  a.n_pages = d->n_pages;
+  a.page_tiles = d->page_tokens / kTile;
+  a.n_kv_heads = d->n_kv_heads;
+  a.bits_k = d->bits_k;
+  a.bits_v = d->bits_v;
+  a.rec_bytes = static_cast<int>(tile_record_bytes(d->bits_k, d->bits_v));
+  a.hdr_bytes = static_cast<int>(header_bytes(d->n_kv_heads));
+  if (s) {
+    if (!s->block_table || !s->seq_lens) return KVQ_ERR_ARG;
+    if (s->batch < 1 || s->batch > kPagedMaxBatch || s->max_pages < 1) return KVQ_ERR_SHAPE;
+    if (s->batch > 1 && s->table_stride < s->max_pages) return KVQ_ERR_ARG;
+    if (static_cast<long long>(s->max_pages) * d->page_tokens > 0x7fffffffLL) return KVQ_ERR_RANGE;   // positions are 32-bit
+    a.block_table = s->block_table;
+    a.seq_lens = s->seq_lens;
+    a.table_stride = s->table_stride;
+    a.batch = s->batch;
+    a.max_pages = s->max_pages;
+  }
+  *out = a;
+  return KVQ_OK;
+}
+
+// Raises a kernel's shared-memory opt-in once per device and context to the largest size asked
+// for so far.
+struct SmemOptIn {
+  std::mutex mu;
+  int set[kMaxDevices] = {};
+  uint64_t ctx[kMaxDevices] = {};
+  template <typename K>
+  kvq_status raise(K kern, size_t smem) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return KVQ_ERR_CUDA;
+    const uint64_t id = context_id();
+    std::lock_guard<std::mutex> lock(mu);
+    if (ctx[dev] == id && set[dev] >= static_cast<int>(smem)) return KVQ_OK;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return cuda_fail(e);
+    set[dev] = static_cast<int>(smem);
+    ctx[dev] = id;
+    return KVQ_OK;
+  }
+};
+
+template <int DT, int BV>
+kvq_status launch_append(const PagedArgs& a, const PagedQuant& p, const RopeArgs& r, long long max_tasks, cudaStream_t s) {
+  static SmemOptIn opt;
+  const size_t smem = append_smem_bytes(DT, a.batch);
+  const kvq_status st = opt.raise(kvq_paged_quant<DT, BV>, smem);
+  if (st != KVQ_OK) return st;
+  constexpr int qw = QTile<DT>::kWarps;
+  const unsigned grid = static_cast<unsigned>(std::min<long long>(sm_count(), (max_tasks + qw - 1) / qw));
+  const cudaError_t e = launch_pdl(kvq_paged_quant<DT, BV>, dim3(grid), dim3(qw * 32), smem, s, a, p, r);
+  return e == cudaSuccess ? launch_status() : cuda_fail(e);
+}
+template <int DT>
+kvq_status launch_append_bv(const PagedArgs& a, const PagedQuant& p, const RopeArgs& r, long long max_tasks, cudaStream_t s) {
+  switch (a.bits_v) {
+    case 1: return launch_append<DT, 1>(a, p, r, max_tasks, s);
+    case 2: return launch_append<DT, 2>(a, p, r, max_tasks, s);
+    case 3: return launch_append<DT, 3>(a, p, r, max_tasks, s);
+    case 4: return launch_append<DT, 4>(a, p, r, max_tasks, s);
+    case 5: return launch_append<DT, 5>(a, p, r, max_tasks, s);
+    case 6: return launch_append<DT, 6>(a, p, r, max_tasks, s);
+    case 7: return launch_append<DT, 7>(a, p, r, max_tasks, s);
+    default: return launch_append<DT, 8>(a, p, r, max_tasks, s);
+  }
+}
+
+// Shares of a paged decode. Own pages: `slots` splits of the whole batch per KV head, one CTA
+// each; with fewer (sequence, KV head) pairs than SMs the slots fill the SMs once, else every
+// pair gets one.
+int paged_slots(int batch, int n_kv_heads) { return std::max(batch, sm_count() / n_kv_heads); }
+
+// Prefix: query rows per CTA (kvq_prefix_gtq's R) and its pipelines.
+struct PrefixPlan {
+  int rows, pipes, groups, splits;
+};
+PrefixPlan prefix_plan(int n_rows, int n_kv_heads) {
+  PrefixPlan p;
+  p.rows = n_rows <= 32 ? 32 : n_rows <= 64 ? 64 : 128;
+  p.pipes = p.rows == 128 ? 1 : 2;
+  p.groups = (n_rows + p.rows - 1) / p.rows;
+  p.splits = std::max(1, sm_count() / (n_kv_heads * p.groups));   // fewer for a prefix of fewer chunks
+  return p;
+}
+
+// Workspace: status word, the plan that the decode leaves to the merge, (m, l, O) of the
+// sequences' own shares, then of the prefix's.
+struct PagedWs {
+  size_t plan, own_m, own_l, own_o, pre_m, pre_l, pre_o, total;
+};
+PagedWs paged_ws(int batch, int n_kv_heads, int group, bool prefix) {
+  PagedWs w;
+  const size_t own = static_cast<size_t>(paged_slots(batch, n_kv_heads)) * n_kv_heads * 8;
+  size_t pre = 0;
+  if (prefix) {
+    const PrefixPlan p = prefix_plan(batch * group, n_kv_heads);
+    pre = static_cast<size_t>(p.splits) * n_kv_heads * p.groups * p.pipes * p.rows;
+  }
+  w.plan = sizeof(WsHeader);
+  w.own_m = align_up(w.plan + sizeof(int2) * batch, 128);
+  w.own_l = align_up(w.own_m + 4 * own, 128);
+  w.own_o = align_up(w.own_l + 4 * own, 128);
+  w.pre_m = align_up(w.own_o + 4 * kD * own, 128);
+  w.pre_l = align_up(w.pre_m + 4 * pre, 128);
+  w.pre_o = align_up(w.pre_l + 4 * pre, 128);
+  w.total = align_up(w.pre_o + 4 * kD * pre, 128);
+  return w;
+}
+
+template <int R, int kPipes>
+kvq_status launch_prefix(PrefixArgs a, cudaStream_t s) {
+  static SmemOptIn opt;
+  const int cb = chunk_bytes(a.pg.rec_bytes) * kPipes;
+  const size_t room = max_smem() - prefix_stage_off<R, kPipes>();
+  a.n_stages = static_cast<int>(std::min<size_t>(kStagesMax, room / cb));
+  if (a.n_stages < 1) return KVQ_ERR_UNSUPPORTED;
+  const size_t smem = prefix_stage_off<R, kPipes>() + static_cast<size_t>(a.n_stages) * cb;
+  const kvq_status st = opt.raise(kvq_prefix_gtq<R, kPipes>, smem);
+  if (st != KVQ_OK) return st;
+  const unsigned grid = static_cast<unsigned>(a.splits * a.row_groups * a.pg.n_kv_heads);
+  const cudaError_t e =
+      launch_pdl(kvq_prefix_gtq<R, kPipes>, dim3(grid), dim3(PrefixCfg<R, kPipes>::kThreads), smem, s, a);
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
+}
+
+template <int VM>
+kvq_status launch_paged_decode(const DecArgs& a, size_t smem, cudaStream_t s) {
+  static SmemOptIn opt;
+  const kvq_status st = opt.raise(kvq_decode_gtq<VM, true>, smem);
+  if (st != KVQ_OK) return st;
+  const unsigned grid = static_cast<unsigned>(a.slots * a.n_kv_heads);
+  const cudaError_t e = launch_pdl(kvq_decode_gtq<VM, true>, dim3(grid), dim3(kDecThreads), smem, s, a);
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+kvq_status kvq_rope(const void* x, const kvq_tensor4* xd, const kvq_rope_desc* rope, void* out, const kvq_tensor4* od,
+                    void* stream) {
+  kvq_status st;
+  if ((st = check_tensor(x, xd)) != KVQ_OK) return st;
+  if ((st = check_tensor(out, od)) != KVQ_OK) return st;
+  if (od->dtype != xd->dtype) return KVQ_ERR_DTYPE;
+  if (od->batch != xd->batch || od->n_heads != xd->n_heads || od->seq_len != xd->seq_len) return KVQ_ERR_SHAPE;
+  if (!rows_apart(od)) return KVQ_ERR_ARG;
+  if (x == out && (od->stride_b != xd->stride_b || od->stride_h != xd->stride_h || od->stride_t != xd->stride_t))
+    return KVQ_ERR_ARG;
+  if (!rope) return KVQ_ERR_ARG;
+  RopeRows a{};
+  a.n_tokens = static_cast<int64_t>(xd->batch) * xd->seq_len;
+  RopeArgs r{};
+  if ((st = rope_args(rope, a.n_tokens, &r)) != KVQ_OK) return st;
+  a.x = static_cast<const uint8_t*>(x);
+  a.out = static_cast<uint8_t*>(out);
+  a.xsb = xd->stride_b;
+  a.xsh = xd->stride_h;
+  a.xst = xd->stride_t;
+  a.osb = od->stride_b;
+  a.osh = od->stride_h;
+  a.ost = od->stride_t;
+  a.seq_len = xd->seq_len;
+  a.n_heads = xd->n_heads;
+  const int64_t token_ctas = (a.n_tokens + rope_cta_tokens(xd->dtype) - 1) / rope_cta_tokens(xd->dtype);
+  if (token_ctas > 0x7fffffffLL) return KVQ_ERR_RANGE;
+  // Few tokens: heads are spread over CTAs until every SM has a few, at the price of reading a
+  // token's cosines again for each group of heads.
+  const int64_t want = std::max<int64_t>(1, 4 * sm_count() / token_ctas);
+  const int per = static_cast<int>(std::max<int64_t>(1, (a.n_heads + want - 1) / want));
+  a.heads_per_cta = (per + kRopeBatch - 1) / kRopeBatch * kRopeBatch;
+  if (per < kRopeBatch) a.heads_per_cta = per;
+  const int64_t head_ctas = (a.n_heads + a.heads_per_cta - 1) / a.heads_per_cta;
+  if (head_ctas > 65535) return KVQ_ERR_RANGE;
+  const dim3 grid(static_cast<unsigned>(token_ctas), static_cast<unsigned>(head_ctas));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  switch (xd->dtype) {
+    case KVQ_F32: e = launch_pdl(kvq_rope_rows<KVQ_F32>, grid, dim3(kRopeThreads), 0, s, a, r); break;
+    case KVQ_F16: e = launch_pdl(kvq_rope_rows<KVQ_F16>, grid, dim3(kRopeThreads), 0, s, a, r); break;
+    default: e = launch_pdl(kvq_rope_rows<KVQ_BF16>, grid, dim3(kRopeThreads), 0, s, a, r); break;
+  }
+  return e == cudaSuccess ? launch_status() : cuda_fail(e);
+}
+
+size_t kvq_paged_bytes(const kvq_paged_desc* d) {
+  if (!paged_ok(d)) return 0;
+  return header_bytes(d->n_kv_heads) + static_cast<size_t>(d->n_pages) * d->n_kv_heads * (d->page_tokens / kTile) *
+                                           tile_record_bytes(d->bits_k, d->bits_v);
+}
+
+kvq_status kvq_paged_init(const void* alloc, const kvq_paged_desc* d, void* pool, void* stream) {
+  PagedArgs a;
+  const kvq_status st = paged_args(d, nullptr, &a);
+  if (st != KVQ_OK) return st;
+  if (!alloc || !pool || !aligned16(alloc) || !aligned16(pool)) return KVQ_ERR_ARG;
+  const cudaError_t e = launch_pdl(kvq_paged_header, dim3(1), dim3(128), 0, static_cast<cudaStream_t>(stream),
+                                   static_cast<uint8_t*>(pool), a, static_cast<const kvq_head_alloc*>(alloc));
+  return e == cudaSuccess ? launch_status() : cuda_fail(e);
+}
+
+kvq_status kvq_paged_append(const void* K, const kvq_tensor4* kd, const void* V, const kvq_tensor4* vd,
+                            const kvq_rope_desc* rope, const void* alloc, const kvq_paged_desc* d,
+                            const kvq_page_table* seqs, const int32_t* cu_tokens, void* pool, void* stream) {
+  kvq_status st;
+  if ((st = check_tensor(K, kd)) != KVQ_OK) return st;
+  if ((st = check_tensor(V, vd)) != KVQ_OK) return st;
+  if (!seqs || !cu_tokens || !alloc || !pool || !aligned16(alloc) || !aligned16(pool)) return KVQ_ERR_ARG;
+  PagedArgs a;
+  if ((st = paged_args(d, seqs, &a)) != KVQ_OK) return st;
+  if (vd->dtype != kd->dtype) return KVQ_ERR_DTYPE;
+  if (kd->batch != 1 || vd->batch != 1 || kd->n_heads != d->n_kv_heads || vd->n_heads != d->n_kv_heads ||
+      vd->seq_len != kd->seq_len)
+    return KVQ_ERR_SHAPE;
+  RopeArgs r{};
+  if (rope && (st = rope_args(rope, kd->seq_len, &r)) != KVQ_OK) return st;
+  if ((st = ensure_tables()) != KVQ_OK) return st;
+  PagedQuant p{};
+  p.K = static_cast<const uint8_t*>(K);
+  p.V = static_cast<const uint8_t*>(V);
+  p.ksh = kd->stride_h;
+  p.kst = kd->stride_t;
+  p.vsh = vd->stride_h;
+  p.vst = vd->stride_t;
+  p.n_tokens = kd->seq_len;
+  p.cu = cu_tokens;
+  p.alloc = static_cast<const kvq_head_alloc*>(alloc);
+  p.pool = static_cast<uint8_t*>(pool);
+  // a sequence's tokens touch at most one tile more than they fill, plus a started one
+  const long long tiles = std::min<long long>(kd->seq_len, kd->seq_len / kTile + 2LL * seqs->batch);
+  const long long tasks = tiles * d->n_kv_heads;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (kd->dtype) {
+    case KVQ_F32: return launch_append_bv<KVQ_F32>(a, p, r, tasks, s);
+    case KVQ_F16: return launch_append_bv<KVQ_F16>(a, p, r, tasks, s);
+    default: return launch_append_bv<KVQ_BF16>(a, p, r, tasks, s);
+  }
+}
+
+size_t kvq_paged_decode_workspace_bytes(const kvq_paged_desc* d, int batch, int n_q_heads, int prefix_len) {
+  if (!paged_ok(d) || batch < 1 || batch > kPagedMaxBatch || n_q_heads < 1 || n_q_heads % d->n_kv_heads != 0 ||
+      n_q_heads / d->n_kv_heads > 8 || prefix_len < 0)
+    return 0;
+  return paged_ws(batch, d->n_kv_heads, n_q_heads / d->n_kv_heads, prefix_len > 0).total;
+}
+
+kvq_status kvq_paged_decode_attn(const void* q, const kvq_tensor4* qd, const void* pool, const void* alloc,
+                                 const kvq_paged_desc* d, const kvq_page_table* seqs, const kvq_prefix* prefix,
+                                 void* out, int out_dtype, void* ws, size_t ws_bytes, void* stream) {
+  kvq_status st;
+  if ((st = check_tensor(q, qd)) != KVQ_OK) return st;
+  if (!pool || !alloc || !seqs || !out || !aligned16(pool) || !aligned16(alloc) || !aligned16(out)) return KVQ_ERR_ARG;
+  if (elem_size(out_dtype) == 0) return KVQ_ERR_DTYPE;
+  PagedArgs pg;
+  if ((st = paged_args(d, seqs, &pg)) != KVQ_OK) return st;
+  if (qd->seq_len != 1 || qd->batch != seqs->batch) return KVQ_ERR_SHAPE;
+  if (qd->n_heads % d->n_kv_heads != 0 || qd->n_heads / d->n_kv_heads > 8) return KVQ_ERR_UNSUPPORTED;
+  const int plen = prefix ? prefix->seq_len : 0;
+  if (plen < 0) return KVQ_ERR_RANGE;
+  if (plen > 0) {
+    if (!prefix->pages) return KVQ_ERR_ARG;
+    if (plen > static_cast<long long>(prefix->n_pages) * d->page_tokens) return KVQ_ERR_RANGE;
+  }
+  const int group = qd->n_heads / d->n_kv_heads;
+  const PagedWs w = paged_ws(seqs->batch, d->n_kv_heads, group, plen > 0);
+  if (!ws || ws_bytes < w.total || !aligned16(ws)) return KVQ_ERR_WORKSPACE;
+  const int cb = chunk_bytes(pg.rec_bytes);
+  const size_t smem = decode_smem_bytes(cb);
+  if (smem > max_smem()) return KVQ_ERR_UNSUPPORTED;
+  if ((st = ensure_tables()) != KVQ_OK) return st;
+  uint8_t* w8 = static_cast<uint8_t*>(ws);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  MergeArgs m{};
+  m.out = out;
+  m.out_dtype = out_dtype;
+  m.n_q_heads = qd->n_heads;
+  m.n_kv_heads = d->n_kv_heads;
+  m.group = group;
+  m.seq_lens = pg.seq_lens;
+  m.plan = reinterpret_cast<const int2*>(w8 + w.plan);
+  m.direct = plen == 0;
+  m.own_m = reinterpret_cast<const float*>(w8 + w.own_m);
+  m.own_l = reinterpret_cast<const float*>(w8 + w.own_l);
+  m.own_o = reinterpret_cast<const float*>(w8 + w.own_o);
+  if (plen > 0) {
+    PrefixPlan pp = prefix_plan(seqs->batch * group, d->n_kv_heads);
+    pp.splits = std::min(pp.splits, (n_tiles_of(plen) + kChunkTiles - 1) / kChunkTiles);
+    PrefixArgs a{};
+    a.q = q;
+    a.qsb = qd->stride_b;
+    a.qsh = qd->stride_h;
+    a.q_dtype = qd->dtype;
+    a.n_rows = seqs->batch * group;
+    a.group = group;
+    a.pool = static_cast<const uint8_t*>(pool);
+    a.alloc = static_cast<const kvq_head_alloc*>(alloc);
+    a.pg = pg;
+    a.pages = prefix->pages;
+    a.len = plen;
+    a.splits = pp.splits;
+    a.row_groups = pp.groups;
+    a.part_m = reinterpret_cast<float*>(w8 + w.pre_m);
+    a.part_l = reinterpret_cast<float*>(w8 + w.pre_l);
+    a.part_o = reinterpret_cast<float*>(w8 + w.pre_o);
+    a.status = reinterpret_cast<unsigned*>(w8);
+    a.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
+    a.debug_no_loads = g_debug_no_loads.load(std::memory_order_relaxed);
+    st = pp.rows == 32 ? launch_prefix<32, 2>(a, s) : pp.rows == 64 ? launch_prefix<64, 2>(a, s) : launch_prefix<128, 1>(a, s);
+    if (st != KVQ_OK) return st;
+    m.prefix_len = plen;
+    m.pre_rows = pp.rows;
+    m.pre_groups = pp.groups;
+    m.pre_splits = pp.splits;
+    m.pre_pipes = pp.pipes;
+    m.pre_m = a.part_m;
+    m.pre_l = a.part_l;
+    m.pre_o = a.part_o;
+  }
+  DecArgs a{};
+  a.q = q;
+  a.qsb = qd->stride_b;
+  a.qsh = qd->stride_h;
+  a.q_dtype = qd->dtype;
+  a.n_q_heads = qd->n_heads;
+  a.n_kv_heads = d->n_kv_heads;
+  a.batch = seqs->batch;
+  a.cbytes = cb;
+  a.packed = static_cast<const uint8_t*>(pool);
+  a.alloc = static_cast<const kvq_head_alloc*>(alloc);
+  a.hdr_bytes = pg.hdr_bytes;
+  a.rec_bytes = pg.rec_bytes;
+  a.bits_k = d->bits_k;
+  a.bits_v = d->bits_v;
+  a.n_stages = decode_stages(cb);
+  a.part_m = reinterpret_cast<float*>(w8 + w.own_m);
+  a.part_l = reinterpret_cast<float*>(w8 + w.own_l);
+  a.part_o = reinterpret_cast<float*>(w8 + w.own_o);
+  a.status = reinterpret_cast<unsigned*>(w8);
+  a.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
+  a.debug_no_loads = g_debug_no_loads.load(std::memory_order_relaxed);
+  a.pg = pg;
+  a.slots = paged_slots(seqs->batch, d->n_kv_heads);
+  a.direct = m.direct;
+  a.out_rows = out;
+  a.out_dtype = out_dtype;
+  a.plan = reinterpret_cast<int2*>(w8 + w.plan);
+  switch (d->bits_v) {
+    case 1: st = launch_paged_decode<1>(a, smem, s); break;
+    case 2: st = launch_paged_decode<2>(a, smem, s); break;
+    case 3: st = launch_paged_decode<3>(a, smem, s); break;
+    case 4: st = launch_paged_decode<4>(a, smem, s); break;
+    case 5: st = launch_paged_decode<5>(a, smem, s); break;
+    case 6: st = launch_paged_decode<6>(a, smem, s); break;
+    case 7: st = launch_paged_decode<7>(a, smem, s); break;
+    default: st = launch_paged_decode<8>(a, smem, s); break;
+  }
+  if (st != KVQ_OK) return st;
+  const cudaError_t e = launch_pdl(kvq_paged_merge, dim3(static_cast<unsigned>(seqs->batch * qd->n_heads)),
+                                   dim3(kMergeWarps * 32), 0, s, m);
+  return e == cudaSuccess ? launch_status() : cuda_fail(e);
 }
 
 }  // extern "C"

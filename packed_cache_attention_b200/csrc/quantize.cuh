@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(QTile<DT>::kWarps * 32, 1) kvq_quant_pack(
 
 // Dynamic shared memory of kvq_quant_pack: the code lookup table, then per warp the K and V
 // tiles, the value scales, the K entry table and the class table.
-inline size_t quant_smem_bytes(int dtype) {
+__host__ __device__ constexpr size_t quant_smem_bytes(int dtype) {
   if (dtype == KVQ_F32) return kLutEntries * 8 + static_cast<size_t>(QTile<KVQ_F32>::kWarps) * QWarpSmem<KVQ_F32>::kBytes;
   return kLutEntries * 8 + static_cast<size_t>(QTile<KVQ_BF16>::kWarps) * QWarpSmem<KVQ_BF16>::kBytes;
 }

@@ -78,11 +78,33 @@ class DecodeExtra(ctypes.Structure):
                 ("V_recent", ctypes.c_void_p), ("vrd", Tensor4)]
 
 
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("axis_stride", ctypes.c_int64),
+                ("n_positions", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("axis", ctypes.c_uint8 * 64)]
+
+
+class PagedDesc(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("bits_k", ctypes.c_int32), ("bits_v", ctypes.c_int32)]
+
+
+class PageTable(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class Prefix(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("seq_len", ctypes.c_int32)]
+
+
 _VP = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _I = ctypes.c_int
 _P4 = ctypes.POINTER(Tensor4)
 _PC = ctypes.POINTER(CacheDesc)
+_PP = ctypes.POINTER(PagedDesc)
+_PR = ctypes.POINTER(RopeDesc)
+_PT = ctypes.POINTER(PageTable)
 
 _SIGNATURES = {
     "kvq_abi_version": ([], _I),
@@ -113,6 +135,12 @@ _SIGNATURES = {
     "kvq_decode_attn_noalloc": ([_VP, _P4, _VP, _VP, _PC, _I, _VP, _VP], _I),
     "kvq_decode_noalloc_scratch_bytes": ([], _SZ),
     "kvq_decode_noalloc_status": ([_VP, ctypes.POINTER(_I)], _I),
+    "kvq_rope": ([_VP, _P4, _PR, _VP, _P4, _VP], _I),
+    "kvq_paged_bytes": ([_PP], _SZ),
+    "kvq_paged_init": ([_VP, _PP, _VP, _VP], _I),
+    "kvq_paged_append": ([_VP, _P4, _VP, _P4, _PR, _VP, _PP, _PT, _VP, _VP, _VP], _I),
+    "kvq_paged_decode_workspace_bytes": ([_PP, _I, _I, _I], _SZ),
+    "kvq_paged_decode_attn": ([_VP, _P4, _VP, _VP, _PP, _PT, ctypes.POINTER(Prefix), _VP, _I, _VP, _SZ, _VP], _I),
 }
 
 _lib = None
@@ -420,6 +448,183 @@ def kvq_nf4_decode_attn(q, packed, capacity: int, seq_len: int, out=None, ws=Non
     _check("kvq_nf4_decode_attn", lib().kvq_nf4_decode_attn(q.data_ptr(), ctypes.byref(qd), packed.data_ptr(),
                                                             capacity, seq_len, out.data_ptr(), ws.data_ptr(),
                                                             ws.numel(), _stream(stream)))
+    return out
+
+
+# ----------------------------------------------------------------------------- rotary positions, paged cache
+
+_DTYPE_CODES: dict = {}
+
+
+def _code_of(dtype) -> int:
+    if not _DTYPE_CODES:
+        torch = _torch()
+        _DTYPE_CODES.update({torch.float32: KVQ_F32, torch.float16: KVQ_F16, torch.bfloat16: KVQ_BF16})
+    if dtype not in _DTYPE_CODES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return _DTYPE_CODES[dtype]
+
+
+def _on_device(first, *rest) -> None:
+    """The calls below launch on the current CUDA device: every tensor has to be there."""
+    dev = first.device
+    if dev.type != "cuda" or dev.index != _torch().cuda.current_device():
+        raise ValueError(f"tensor on {dev}, not on the current CUDA device")
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+
+
+def _ints(t, name: str, *shape) -> int:
+    """Address of an int32 tensor of this shape (None: any size) with adjacent innermost elements."""
+    if t.dtype != _torch().int32:
+        raise ValueError(f"{name} must be int32, not {t.dtype}")
+    got = t.shape
+    if len(got) != len(shape) or any(w is not None and g != w for g, w in zip(got, shape)):
+        raise ValueError(f"{name} has shape {tuple(got)}, expected {shape}")
+    if got[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have adjacent innermost elements")
+    return t.data_ptr()
+
+
+def _bytes(t, name: str, need: int) -> int:
+    if t.element_size() != 1 or not t.is_contiguous() or t.numel() < need:
+        raise ValueError(f"{name} must be {need} contiguous bytes or more")
+    return t.data_ptr()
+
+
+def _rows(t) -> Tensor4:
+    """View of token rows [tokens][heads][128] as one sequence, or of [B][H][T][128] as it is."""
+    st = t.stride()
+    if t.shape[-1] > 1 and st[-1] != 1:
+        raise ValueError("last dimension must be contiguous")
+    if t.dim() == 3:
+        n, h, d = t.shape
+        return Tensor4(1, h, n, d, 0, st[1], st[0], _code_of(t.dtype), 0)
+    if t.dim() != 4:
+        raise ValueError("expected [tokens][heads][128] or [batch][heads][tokens][128]")
+    B, h, n, d = t.shape
+    return Tensor4(B, h, n, d, st[0], st[1], st[2], _code_of(t.dtype), 0)
+
+
+def rope_desc(table, positions, axis=None) -> RopeDesc:
+    """Rotation of block b by the angle of position positions[axis[b]][token]: table fp32
+    [n_positions][64][2] of (cos, sin), positions int32 [n_axes][tokens] (or [tokens] for one axis), axis a
+    sequence of 64 axis numbers (None: all 0). Keeps the tensors alive."""
+    if table.dtype != _torch().float32 or table.dim() != 3 or table.shape[1:] != (64, 2) or not table.is_contiguous():
+        raise ValueError("table must be contiguous fp32 [n_positions][64][2]")
+    if positions.dim() == 1:
+        positions = positions[None]
+    r = RopeDesc(table.data_ptr(), _ints(positions, "positions", None, None), positions.stride(0), table.shape[0],
+                 positions.shape[0])
+    if axis is not None:
+        if len(axis) != 64:
+            raise ValueError("axis needs 64 entries")
+        r.axis[:] = axis
+    r.tensors = (table, positions)
+    return r
+
+
+def _rope_tokens(rope, n: int) -> None:
+    if rope.tensors[1].shape[1] < n:
+        raise ValueError(f"{rope.tensors[1].shape[1]} positions for {n} tokens")
+
+
+def kvq_rope(x, rope: RopeDesc, out=None, stream=None):
+    """x [tokens][heads][128] or [B][H][T][128] rotated (token b * T + t has position index b * T + t); out may
+    be x."""
+    torch = _torch()
+    _on_device(x, out, *rope.tensors)
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif out.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    xd, od = _rows(x), _rows(out)
+    _rope_tokens(rope, xd.batch * xd.seq_len)
+    _check("kvq_rope", lib().kvq_rope(x.data_ptr(), ctypes.byref(xd), ctypes.byref(rope), out.data_ptr(),
+                                      ctypes.byref(od), _stream(stream)))
+    return out
+
+
+def paged_desc(n_pages: int, page_tokens: int, n_kv_heads: int, bits_k: int, bits_v: int, head_dim: int = HEAD_DIM):
+    return PagedDesc(n_pages, page_tokens, n_kv_heads, head_dim, bits_k, bits_v)
+
+
+def kvq_paged_bytes(desc: PagedDesc) -> int:
+    return lib().kvq_paged_bytes(ctypes.byref(desc))
+
+
+def kvq_paged_decode_workspace_bytes(desc: PagedDesc, batch: int, n_q_heads: int, prefix_len: int = 0) -> int:
+    return lib().kvq_paged_decode_workspace_bytes(ctypes.byref(desc), batch, n_q_heads, prefix_len)
+
+
+def kvq_paged_decode_workspace(desc: PagedDesc, batch: int, n_q_heads: int, prefix_len: int = 0, device=None):
+    """A zeroed workspace for kvq_paged_decode_attn."""
+    n = kvq_paged_decode_workspace_bytes(desc, batch, n_q_heads, prefix_len)
+    if n == 0:
+        raise ValueError("no workspace for these sizes")
+    return _torch().zeros(n, dtype=_torch().uint8, device="cuda" if device is None else device)
+
+
+def kvq_paged_init(alloc, desc: PagedDesc, pool=None, stream=None):
+    """Writes the header of a pool (uint8 device tensor, made if None); its pages stay as they are."""
+    if pool is None:
+        pool = _empty_bytes(kvq_paged_bytes(desc), alloc.device)
+    _on_device(alloc, pool)
+    _check("kvq_paged_init", lib().kvq_paged_init(_bytes(alloc, "alloc", kvq_alloc_bytes(desc.n_kv_heads)),
+                                                  ctypes.byref(desc), _bytes(pool, "pool", kvq_paged_bytes(desc)),
+                                                  _stream(stream)))
+    return pool
+
+
+def _page_table(block_table, seq_lens) -> PageTable:
+    batch = block_table.shape[0]
+    return PageTable(_ints(block_table, "block_table", batch, None), _ints(seq_lens, "seq_lens", batch),
+                     block_table.stride(0), batch, block_table.shape[1])
+
+
+def kvq_paged_append(K, V, alloc, desc: PagedDesc, block_table, seq_lens, cu_tokens, pool, rope: RopeDesc | None = None,
+                     stream=None):
+    """Rows cu_tokens[b] .. cu_tokens[b + 1] - 1 of K, V [tokens][Hkv][128] become positions seq_lens[b] .. of
+    sequence b (pages block_table[b], int32), keys rotated by `rope` first. seq_lens is left as it is."""
+    _on_device(K, V, alloc, block_table, seq_lens, cu_tokens, pool, *(rope.tensors if rope is not None else ()))
+    kd, vd = _rows(K), _rows(V)
+    seqs = _page_table(block_table, seq_lens)
+    if rope is not None:
+        _rope_tokens(rope, kd.seq_len)
+    _check("kvq_paged_append", lib().kvq_paged_append(
+        K.data_ptr(), ctypes.byref(kd), V.data_ptr(), ctypes.byref(vd), ctypes.byref(rope) if rope is not None else None,
+        _bytes(alloc, "alloc", kvq_alloc_bytes(desc.n_kv_heads)), ctypes.byref(desc), ctypes.byref(seqs),
+        _ints(cu_tokens, "cu_tokens", seqs.batch + 1), _bytes(pool, "pool", kvq_paged_bytes(desc)), _stream(stream)))
+    return pool
+
+
+def kvq_paged_decode_attn(q, pool, alloc, desc: PagedDesc, block_table, seq_lens, prefix_pages=None, prefix_len: int = 0,
+                          out_dtype=None, out=None, ws=None, stream=None):
+    """Decode attention of q [B][Hq][128] over each sequence's pages, after a prefix that the whole batch shares
+    (prefix_pages int32 [pages], prefix_len positions); returns out [B][Hq][128] (fp32 unless out_dtype says)."""
+    torch = _torch()
+    B, Hq, d = q.shape
+    _on_device(q, pool, alloc, block_table, seq_lens, prefix_pages, out, ws)
+    if out is None:
+        out = torch.empty((B, Hq, d), dtype=torch.float32 if out_dtype is None else out_dtype, device=q.device)
+    elif out.shape != q.shape or not out.is_contiguous() or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out must be contiguous, of q's shape and of out_dtype")
+    if ws is None:
+        ws = kvq_paged_decode_workspace(desc, B, Hq, prefix_len, q.device)
+    if q.stride(2) != 1:
+        raise ValueError("last dimension must be contiguous")
+    qd = Tensor4(B, Hq, 1, d, q.stride(0), q.stride(1), d, _code_of(q.dtype), 0)
+    seqs = _page_table(block_table, seq_lens)
+    prefix = None
+    if prefix_len:
+        if prefix_pages is None:
+            raise ValueError("a prefix needs its pages")
+        prefix = ctypes.byref(Prefix(_ints(prefix_pages, "prefix_pages", None), prefix_pages.shape[0], prefix_len))
+    _check("kvq_paged_decode_attn", lib().kvq_paged_decode_attn(
+        q.data_ptr(), ctypes.byref(qd), _bytes(pool, "pool", kvq_paged_bytes(desc)),
+        _bytes(alloc, "alloc", kvq_alloc_bytes(desc.n_kv_heads)), ctypes.byref(desc), ctypes.byref(seqs), prefix,
+        out.data_ptr(), _code_of(out.dtype), _bytes(ws, "ws", 0), ws.numel(), _stream(stream)))
     return out
 
 

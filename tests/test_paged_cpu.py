@@ -1,0 +1,216 @@
+"""Rotary positions and the paged cache without a GPU: struct layouts, sizes, and the calls that
+are refused before anything is launched."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+from oracle import blockgtq as bg
+from oracle import rope as orope
+from packed_cache_attention_b200 import kvq
+from tests import test_c_client as cc
+from tests.paged_util import angle_table, rotate_f32
+from tests.test_abi import L, WS_BYTES, _t4, buf  # noqa: F401
+
+ARG, SHAPE, DTYPE, RANGE, WORKSPACE, UNSUPPORTED = 1, 2, 3, 5, 6, 9
+
+
+def test_structs_have_the_headers_layout(tmp_path, monkeypatch):
+    structs = [("kvq_rope_desc", kvq.RopeDesc), ("kvq_paged_desc", kvq.PagedDesc), ("kvq_page_table", kvq.PageTable),
+               ("kvq_prefix", kvq.Prefix)]
+    monkeypatch.setattr(cc, "STRUCTS", structs)
+    cc.test_binding_structs_have_the_headers_layout(tmp_path)
+
+
+def test_sizes_follow_the_layout(L):
+    for (n, page, h, bk, bv) in [(1, 32, 1, 1, 1), (10, 64, 2, 3, 3), (7, 256, 8, 4, 5), (3, 65536, 9, 8, 8)]:
+        want = bg.header_bytes(h) + n * h * (page // 32) * bg.tile_record_bytes(128, bk, bv)
+        assert kvq.kvq_paged_bytes(kvq.paged_desc(n, page, h, bk, bv)) == want
+    for bad in [(0, 64, 2, 3, 3), (4, 33, 2, 3, 3), (4, 0, 2, 3, 3), (4, 65568, 2, 3, 3), (4, 64, 0, 3, 3), (4, 64, 2, 0, 3),
+                (4, 64, 2, 9, 3), (4, 64, 2, 3, 0), (4, 64, 2, 3, 9), (4, 64, 2, 3, 3, 64)]:
+        assert kvq.kvq_paged_bytes(kvq.paged_desc(*bad)) == 0, bad
+    d = kvq.paged_desc(100, 64, 2, 3, 3)
+    ws = lambda *a: kvq.kvq_paged_decode_workspace_bytes(d, *a)  # noqa: E731
+    assert ws(4, 16, 100) > ws(4, 16, 0) > 0
+    assert ws(4, 16, 1) == ws(4, 16, 131072)                              # any length
+    for bad in [(0, 16, 0), (1025, 16, 0), (4, 15, 0), (4, 18, 0), (4, 0, 0), (4, 16, -1)]:
+        assert ws(*bad) == 0, bad
+    assert ws(1024, 16, 100) > 0
+    with pytest.raises(ValueError):
+        kvq.kvq_paged_decode_workspace(d, 0, 16, 0, "cpu")
+
+
+def test_plain_rotation_is_the_rotation_of_the_formula():
+    """The tests' fp32 rotation against the complex rotation in 64 bits, three axes."""
+    rng = np.random.default_rng(5)
+    x = rng.standard_normal((9, 3, 128)).astype(np.float32)
+    axis = np.minimum((np.arange(64) + 8) // 24, 2)
+    pos = rng.integers(0, 500, (3, 9))
+    got = rotate_f32(x, angle_table(500), pos, axis)
+    for t in range(9):
+        for h in range(3):
+            for a in range(3):
+                r = orope.rotate(x[t, h], float(pos[a, t]), 1e6)
+                dims = np.concatenate([np.flatnonzero(axis == a), np.flatnonzero(axis == a) + 64])
+                scale = np.abs(x[t, h]).max()
+                assert np.abs(got[t, h, dims] - r[dims]).max() <= 8 * 2.0 ** -24 * scale
+
+
+def _rope(mem, n_pos=16, n_axes=1, stride=64, **kw):
+    r = kvq.RopeDesc(mem, mem, stride, n_pos, n_axes)
+    for k, v in kw.items():
+        setattr(r, k, v)
+    return r
+
+
+def test_rope_refusals(L):
+    mem = buf()
+    out = buf()
+    call = lambda xd, r, od=None, o=None, x=None: L.kvq_rope(  # noqa: E731
+        mem if x is None else x, ctypes.byref(xd), ctypes.byref(r) if r else None, out if o is None else o,
+        ctypes.byref(xd if od is None else od), None)
+    x = _t4(T=8)
+    assert call(x, None) == ARG
+    assert call(_t4(T=0), _rope(mem)) == SHAPE
+    assert call(_t4(T=8, d=64), _rope(mem)) == SHAPE
+    assert call(_t4(T=8, dtype=5), _rope(mem)) == DTYPE
+    assert call(x, _rope(mem), od=_t4(T=8, dtype=kvq.KVQ_F16)) == DTYPE
+    assert call(x, _rope(mem), od=_t4(T=8, H=1)) == SHAPE
+    assert call(x, _rope(mem), o=out + 8) == ARG                           # misaligned
+    assert call(x, _rope(mem), od=_t4(T=8, sh=0)) == ARG                   # two heads written to one place
+    assert call(x, _rope(mem), od=_t4(T=8, sh=64)) == ARG                  # rows overlap
+    assert call(x, _rope(mem), od=_t4(T=8, st=256, sh=128), o=mem) == ARG  # in place with other strides
+    assert call(x, _rope(0)) == ARG
+    assert call(x, _rope(mem, table=mem + 8)) == ARG
+    assert call(x, _rope(mem, n_pos=0)) == SHAPE
+    assert call(x, _rope(mem, n_axes=0)) == SHAPE
+    assert call(x, _rope(mem, n_axes=5)) == SHAPE
+    assert call(x, _rope(mem, n_axes=2, stride=7)) == ARG                  # axes' positions overlap
+    r = _rope(mem)
+    r.axis[63] = 1
+    assert call(x, r) == ARG                                               # axis 1 of one
+
+
+def _pages(mem, batch=2, max_pages=4, stride=None, **kw):
+    t = kvq.PageTable(mem, mem, max_pages if stride is None else stride, batch, max_pages)
+    for k, v in kw.items():
+        setattr(t, k, v)
+    return t
+
+
+D = kvq.paged_desc(8, 64, 2, 3, 3)
+
+
+def test_init_refusals(L):
+    mem = buf()
+    init = lambda a, d, p: L.kvq_paged_init(a, ctypes.byref(d) if d else None, p, None)  # noqa: E731
+    assert init(mem, None, mem) == ARG
+    assert init(mem, kvq.paged_desc(8, 48, 2, 3, 3), mem) == ARG
+    assert init(None, D, mem) == ARG
+    assert init(mem, D, None) == ARG
+    assert init(mem, D, mem + 8) == ARG
+
+
+def test_append_refusals(L):
+    mem = buf()
+
+    def call(kd=None, vd=None, rope=None, d=D, seqs=None, cu=mem, pool=mem, alloc=mem, K=mem):
+        kd = _t4(T=10) if kd is None else kd
+        vd = kd if vd is None else vd
+        seqs = _pages(mem) if seqs is None else seqs
+        return L.kvq_paged_append(K, ctypes.byref(kd), mem, ctypes.byref(vd), ctypes.byref(rope) if rope else None, alloc,
+                                  ctypes.byref(d), ctypes.byref(seqs), cu, pool, None)
+    assert call(K=None) == ARG
+    assert call(kd=_t4(T=0)) == SHAPE
+    assert call(kd=_t4(T=10, B=2)) == SHAPE
+    assert call(kd=_t4(T=10, H=3)) == SHAPE
+    assert call(vd=_t4(T=9)) == SHAPE
+    assert call(vd=_t4(T=10, dtype=kvq.KVQ_F16)) == DTYPE
+    assert call(kd=_t4(T=10, st=132)) == ARG
+    assert call(cu=None) == ARG and call(pool=None) == ARG and call(alloc=None) == ARG
+    assert call(pool=mem + 4) == ARG
+    assert call(d=kvq.paged_desc(8, 64, 2, 3, 0)) == ARG
+    for bad in (dict(batch=0), dict(batch=1025), dict(max_pages=0)):
+        assert call(seqs=_pages(mem, **bad)) == SHAPE
+    assert call(seqs=_pages(mem, stride=3)) == ARG                        # table rows overlap
+    assert call(seqs=_pages(mem, batch=1, max_pages=1 << 26)) == RANGE    # positions are 32-bit
+    assert call(seqs=_pages(mem, block_table=None)) == ARG
+    assert call(seqs=_pages(mem, seq_lens=None)) == ARG
+    assert call(rope=_rope(mem, n_axes=3, stride=9)) == ARG
+    assert call(rope=_rope(mem, n_pos=0)) == SHAPE
+
+
+def test_decode_refusals(L):
+    mem, ws = buf(), buf(WS_BYTES)
+
+    def call(qd=None, d=D, seqs=None, prefix=None, out=mem, dtype=0, w=ws, wsb=WS_BYTES, pool=mem):
+        qd = kvq.Tensor4(2, 16, 1, 128, 2048, 128, 128, kvq.KVQ_BF16, 0) if qd is None else qd
+        seqs = _pages(mem) if seqs is None else seqs
+        return L.kvq_paged_decode_attn(mem, ctypes.byref(qd), pool, mem, ctypes.byref(d), ctypes.byref(seqs),
+                                       ctypes.byref(prefix) if prefix else None, out, dtype, w, wsb, None)
+    assert call(qd=kvq.Tensor4(3, 16, 1, 128, 2048, 128, 128, 2, 0)) == SHAPE       # another batch
+    assert call(qd=kvq.Tensor4(2, 16, 2, 128, 4096, 256, 128, 2, 0)) == SHAPE       # two tokens
+    assert call(qd=kvq.Tensor4(2, 15, 1, 128, 2048, 128, 128, 2, 0)) == UNSUPPORTED
+    assert call(qd=kvq.Tensor4(2, 18, 1, 128, 2304, 128, 128, 2, 0)) == UNSUPPORTED  # 9 heads a KV head
+    assert call(pool=None) == ARG and call(out=None) == ARG and call(out=mem + 4) == ARG
+    assert call(dtype=3) == DTYPE and call(dtype=-1) == DTYPE
+    assert call(d=kvq.paged_desc(8, 64, 2, 3, 0)) == ARG
+    assert call(seqs=_pages(mem, batch=0)) == SHAPE
+    assert call(prefix=kvq.Prefix(mem, 2, -1)) == RANGE
+    assert call(prefix=kvq.Prefix(mem, 2, 129)) == RANGE                            # longer than its pages
+    assert call(prefix=kvq.Prefix(None, 2, 100)) == ARG
+    assert call(w=None) == WORKSPACE and call(wsb=1 << 10) == WORKSPACE
+    need = kvq.kvq_paged_decode_workspace_bytes(D, 2, 16, 100)
+    assert call(prefix=kvq.Prefix(mem, 2, 100), wsb=need - 1) == WORKSPACE
+
+
+def test_binding_refuses_host_tensors_and_wrong_arguments(L):
+    import torch
+    table = torch.from_numpy(angle_table(16))
+    pos = torch.zeros(4, dtype=torch.int32)
+    r = kvq.rope_desc(table, pos)
+    with pytest.raises(ValueError, match="device"):
+        kvq.kvq_rope(torch.zeros(4, 2, 128), r)
+    with pytest.raises(ValueError):
+        kvq.rope_desc(table.double(), pos)
+    with pytest.raises(ValueError):
+        kvq.rope_desc(table, pos.long())
+    with pytest.raises(ValueError):
+        kvq.rope_desc(table, pos, [0] * 63)
+    with pytest.raises(ValueError):
+        kvq.rope_desc(table.transpose(1, 2), pos)
+    with pytest.raises(ValueError):
+        kvq._ints(torch.zeros(3, 8, dtype=torch.int32)[:, ::2], "block_table", 3, None)
+    with pytest.raises(ValueError):
+        kvq._bytes(torch.zeros(10, dtype=torch.uint8), "pool", 11)
+    with pytest.raises(ValueError):
+        kvq._rows(torch.zeros(4, 128))
+    with pytest.raises(ValueError):
+        kvq._rope_tokens(r, 5)
+    z = torch.zeros(2, 4, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        kvq.kvq_paged_decode_attn(torch.zeros(2, 16, 128), torch.zeros(8, dtype=torch.uint8),
+                                  torch.zeros(8, dtype=torch.uint8), D, z, z[:, 0])
+
+
+def test_every_split_rule_covers_the_batch():
+    """The rule that shares a ragged batch out: for any lengths the rounds it settles on fit the slots, no
+    sequence's split is empty, and no CTA gets more rounds than the longest sequence needs alone."""
+    rng = np.random.default_rng(1)
+    for _ in range(300):
+        n = int(rng.integers(1, 70))
+        chunks = rng.integers(0, int(rng.integers(1, 2000)), n)
+        slots = max(n, int(rng.integers(1, 148)))
+        least = max(1, -(-int(chunks.sum()) // (4 * slots)))
+        most = max(1, -(-int(chunks.max()) // 4))
+        tries = [least + -(-least * w // 8) for w in range(19)] + [most]
+        fits = [p for p in tries if sum(-(-int(c) // (4 * p)) for c in chunks) <= slots]
+        best = min(fits)
+        splits = [-(-int(c) // (4 * best)) for c in chunks]
+        assert sum(splits) <= slots and best <= max(most, least * 4)
+        for c, s in zip(chunks, splits):
+            assert (s == 0) == (c == 0)
+            for i in range(s):
+                assert (i + 1) * int(c) // s > i * int(c) // s
+        assert math.isfinite(best)
