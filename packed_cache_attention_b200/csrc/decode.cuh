@@ -1136,7 +1136,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_decode_gtq(const DecArgs a
 #pragma unroll
     for (int gg = 0; gg <= kDecWG; ++gg) {
       if (S.wg_m[gg][h] == -INFINITY) {
-        if (kPaged && S.wg_l[gg][h] != S.wg_l[gg][h]) Ls = S.wg_l[gg][h];   // NaN logits alone
+        if (kPaged && gg < kDecWG && S.wg_l[gg][h] != S.wg_l[gg][h]) Ls = S.wg_l[gg][h];   // NaN logits alone
         continue;
       }
       const float w = fast_exp2(S.wg_m[gg][h] - Mx);

@@ -5,7 +5,7 @@ import pytest
 from oracle import blockgtq as bg
 from packed_cache_attention_b200 import kvq
 from tests.paged_util import Paged, angle_table, check_rows, rotate_f32
-from tests.parity_util import host_f32
+from tests.parity_util import TOL, host_f32, rel_err
 
 pytestmark = pytest.mark.gpu
 ERR_RANGE = 5
@@ -506,6 +506,26 @@ def test_a_paged_cache_answers_as_a_contiguous_one(dev):
     ref, bound = P.attention(q, [n, n])
     check_rows(P.decode(q, [n, n]), ref, bound, torch.float32)
     check_rows(kvq.kvq_decode_attn(q, packed, P.alloc, cache, n), ref, bound, torch.float32)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_long_contexts_agree_with_the_contiguous_decode(dev, seed):
+    """More chunks per warpgroup than copies in flight; each kernel is within its tolerance of the exact rows."""
+    import torch
+    n = 60000 + 117 * seed
+    P = Paged(dev, 30 + seed, 2, 3, 3, 256, [n], prefix=256 * 100)
+    K, V = P.rows(n, torch.bfloat16)
+    P.append(K, V, [0], [0, n])
+    cache = kvq.cache_desc(1, 2, n, 3, 3)
+    packed = kvq.kvq_quantize(*(x.transpose(0, 1)[None].contiguous() for x in (K, V)), P.alloc, cache)
+    q = torch.randn((1, 16, 128), device=dev).to(torch.bfloat16)
+    want = host_f32(kvq.kvq_decode_attn(q, packed, P.alloc, cache, n))
+    assert rel_err(host_f32(P.decode(q, [n])), want) <= 2 * TOL
+    # the first 100 pages as a shared prefix, the others as the sequence's own
+    lead = P.table[0, :100].contiguous()
+    got = kvq.kvq_paged_decode_attn(q, P.pool, P.alloc, P.desc, P.table[:, 100:].contiguous(), P.ints([n - 25600]), prefix_pages=lead,
+                                    prefix_len=25600)
+    assert rel_err(host_f32(got), want) <= 2 * TOL
 
 
 def test_binding_refuses_mixed_arguments(dev):
