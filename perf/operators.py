@@ -480,7 +480,9 @@ def _own(s):
     c = s["case"]
     rope = None
     if c.get("axes"):
-        rope = kvq.rope_desc(s["table"], s["positions"], s.setdefault("axis_list", s["axis"].tolist()))
+        if "axis_list" not in s:
+            s["axis_list"] = s["axis"].tolist()
+        rope = kvq.rope_desc(s["table"], s["positions"], s["axis_list"])
     if c["op"] == "rope":
         return kvq.kvq_rope(s["x"], rope)
     desc = kvq.paged_desc(s["n_pages"], c["page"], c["hkv"], c["bits_k"], c["bits_v"])
