@@ -465,24 +465,31 @@ def _code_of(dtype) -> int:
     return _DTYPE_CODES[dtype]
 
 
-def _on_device(first, *rest) -> None:
-    """The calls below launch on the current CUDA device: every tensor has to be there."""
-    dev = first.device
-    if dev.type != "cuda" or dev.index != _torch().cuda.current_device():
-        raise ValueError(f"tensor on {dev}, not on the current CUDA device")
+def _on_device(first, *rest) -> int:
+    """The calls below launch on the current CUDA device: every tensor has to be there. Returns its index."""
+    dev = first.get_device()
+    if dev < 0 or dev != _torch().cuda.current_device():
+        raise ValueError(f"tensor on {first.device}, not on the current CUDA device")
     for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    return dev
 
 
-def _ints(t, name: str, *shape) -> int:
-    """Address of an int32 tensor of this shape (None: any size) with adjacent innermost elements."""
-    if t.dtype != _torch().int32:
+def _stream_of(stream, dev: int) -> int:
+    """Handle of `stream`, or of the device's current stream (without making a Stream object)."""
+    return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _ints(t, name: str, rows, n) -> int:
+    """Address of an int32 tensor [n] (rows -1) or [rows][n] with adjacent innermost elements; None: any size."""
+    if t.dtype is not _torch().int32:
         raise ValueError(f"{name} must be int32, not {t.dtype}")
-    got = t.shape
-    if len(got) != len(shape) or any(w is not None and g != w for g, w in zip(got, shape)):
-        raise ValueError(f"{name} has shape {tuple(got)}, expected {shape}")
-    if got[-1] > 1 and t.stride(-1) != 1:
+    got, st = t.shape, t.stride()
+    if len(got) != (1 if rows == -1 else 2) or (n is not None and got[-1] != n) or \
+            (rows is not None and rows >= 0 and got[0] != rows):
+        raise ValueError(f"{name} has shape {tuple(got)}, expected {[n] if rows == -1 else [rows, n]}")
+    if st[-1] != 1 and got[-1] > 1:
         raise ValueError(f"{name} must have adjacent innermost elements")
     return t.data_ptr()
 
@@ -520,7 +527,7 @@ def rope_desc(table, positions, axis=None) -> RopeDesc:
     if axis is not None:
         if len(axis) != 64:
             raise ValueError("axis needs 64 entries")
-        r.axis[:] = axis
+        ctypes.memmove(ctypes.addressof(r) + RopeDesc.axis.offset, bytes(axis), 64)
     r.tensors = (table, positions)
     return r
 
@@ -534,15 +541,16 @@ def kvq_rope(x, rope: RopeDesc, out=None, stream=None):
     """x [tokens][heads][128] or [B][H][T][128] rotated (token b * T + t has position index b * T + t); out may
     be x."""
     torch = _torch()
-    _on_device(x, out, *rope.tensors)
+    dev = _on_device(x, out, *rope.tensors)
+    xd = _rows(x)
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif out.shape != x.shape:
         raise ValueError("out must have x's shape")
-    xd, od = _rows(x), _rows(out)
+    od = xd if out is x else _rows(out)
     _rope_tokens(rope, xd.batch * xd.seq_len)
     _check("kvq_rope", lib().kvq_rope(x.data_ptr(), ctypes.byref(xd), ctypes.byref(rope), out.data_ptr(),
-                                      ctypes.byref(od), _stream(stream)))
+                                      ctypes.byref(od), _stream_of(stream, dev)))
     return out
 
 
@@ -570,24 +578,24 @@ def kvq_paged_init(alloc, desc: PagedDesc, pool=None, stream=None):
     """Writes the header of a pool (uint8 device tensor, made if None); its pages stay as they are."""
     if pool is None:
         pool = _empty_bytes(kvq_paged_bytes(desc), alloc.device)
-    _on_device(alloc, pool)
+    dev = _on_device(alloc, pool)
     _check("kvq_paged_init", lib().kvq_paged_init(_bytes(alloc, "alloc", kvq_alloc_bytes(desc.n_kv_heads)),
                                                   ctypes.byref(desc), _bytes(pool, "pool", kvq_paged_bytes(desc)),
-                                                  _stream(stream)))
+                                                  _stream_of(stream, dev)))
     return pool
 
 
 def _page_table(block_table, seq_lens) -> PageTable:
-    batch = block_table.shape[0]
-    return PageTable(_ints(block_table, "block_table", batch, None), _ints(seq_lens, "seq_lens", batch),
-                     block_table.stride(0), batch, block_table.shape[1])
+    table = _ints(block_table, "block_table", None, None)
+    batch, max_pages = block_table.shape
+    return PageTable(table, _ints(seq_lens, "seq_lens", -1, batch), block_table.stride(0), batch, max_pages)
 
 
 def kvq_paged_append(K, V, alloc, desc: PagedDesc, block_table, seq_lens, cu_tokens, pool, rope: RopeDesc | None = None,
                      stream=None):
     """Rows cu_tokens[b] .. cu_tokens[b + 1] - 1 of K, V [tokens][Hkv][128] become positions seq_lens[b] .. of
     sequence b (pages block_table[b], int32), keys rotated by `rope` first. seq_lens is left as it is."""
-    _on_device(K, V, alloc, block_table, seq_lens, cu_tokens, pool, *(rope.tensors if rope is not None else ()))
+    dev = _on_device(K, V, alloc, block_table, seq_lens, cu_tokens, pool, *(rope.tensors if rope is not None else ()))
     kd, vd = _rows(K), _rows(V)
     seqs = _page_table(block_table, seq_lens)
     if rope is not None:
@@ -595,7 +603,8 @@ def kvq_paged_append(K, V, alloc, desc: PagedDesc, block_table, seq_lens, cu_tok
     _check("kvq_paged_append", lib().kvq_paged_append(
         K.data_ptr(), ctypes.byref(kd), V.data_ptr(), ctypes.byref(vd), ctypes.byref(rope) if rope is not None else None,
         _bytes(alloc, "alloc", kvq_alloc_bytes(desc.n_kv_heads)), ctypes.byref(desc), ctypes.byref(seqs),
-        _ints(cu_tokens, "cu_tokens", seqs.batch + 1), _bytes(pool, "pool", kvq_paged_bytes(desc)), _stream(stream)))
+        _ints(cu_tokens, "cu_tokens", -1, seqs.batch + 1), _bytes(pool, "pool", kvq_paged_bytes(desc)),
+        _stream_of(stream, dev)))
     return pool
 
 
@@ -605,26 +614,27 @@ def kvq_paged_decode_attn(q, pool, alloc, desc: PagedDesc, block_table, seq_lens
     (prefix_pages int32 [pages], prefix_len positions); returns out [B][Hq][128] (fp32 unless out_dtype says)."""
     torch = _torch()
     B, Hq, d = q.shape
-    _on_device(q, pool, alloc, block_table, seq_lens, prefix_pages, out, ws)
+    dev = _on_device(q, pool, alloc, block_table, seq_lens, prefix_pages, out, ws)
     if out is None:
         out = torch.empty((B, Hq, d), dtype=torch.float32 if out_dtype is None else out_dtype, device=q.device)
     elif out.shape != q.shape or not out.is_contiguous() or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be contiguous, of q's shape and of out_dtype")
     if ws is None:
         ws = kvq_paged_decode_workspace(desc, B, Hq, prefix_len, q.device)
-    if q.stride(2) != 1:
+    qs = q.stride()
+    if qs[2] != 1:
         raise ValueError("last dimension must be contiguous")
-    qd = Tensor4(B, Hq, 1, d, q.stride(0), q.stride(1), d, _code_of(q.dtype), 0)
+    qd = Tensor4(B, Hq, 1, d, qs[0], qs[1], d, _code_of(q.dtype), 0)
     seqs = _page_table(block_table, seq_lens)
     prefix = None
     if prefix_len:
         if prefix_pages is None:
             raise ValueError("a prefix needs its pages")
-        prefix = ctypes.byref(Prefix(_ints(prefix_pages, "prefix_pages", None), prefix_pages.shape[0], prefix_len))
+        prefix = ctypes.byref(Prefix(_ints(prefix_pages, "prefix_pages", -1, None), prefix_pages.shape[0], prefix_len))
     _check("kvq_paged_decode_attn", lib().kvq_paged_decode_attn(
         q.data_ptr(), ctypes.byref(qd), _bytes(pool, "pool", kvq_paged_bytes(desc)),
         _bytes(alloc, "alloc", kvq_alloc_bytes(desc.n_kv_heads)), ctypes.byref(desc), ctypes.byref(seqs), prefix,
-        out.data_ptr(), _code_of(out.dtype), _bytes(ws, "ws", 0), ws.numel(), _stream(stream)))
+        out.data_ptr(), _code_of(out.dtype), _bytes(ws, "ws", 0), ws.numel(), _stream_of(stream, dev)))
     return out
 
 
