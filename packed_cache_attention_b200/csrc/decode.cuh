@@ -48,7 +48,6 @@
 #pragma once
 
 #include "common.cuh"
-#include "paged_pool.cuh"
 #include "tcgen05.cuh"
 
 namespace kvq {
@@ -121,11 +120,6 @@ struct DecHeader {
   float rx_m[4][8];                    // recent tokens: per issuer warp maximum
   float rx_l[4][8];                    //                                and row sum
   int last;                            // this CTA drew the last ticket of its merge group
-  // paged caches: this CTA's share of the batch
-  int job_seq, job_len, job_split, job_splits;
-  int job_chunks_wg[kDecThreads / 32]; // per warp: a feasible number of chunks per warpgroup
-  int scan[kDecThreads / 32];
-  int bad_page;                        // a page outside the pool: the CTA's result is not used
   uint4 kdesc[kPlanSlots];             // per plan slot of width <= 5: word offset, shifts, mask, stride
   uint32_t kbase[kPlanSlots];          //                                 pair-table byte offset
   int bkind[kPlanSlots / 4];           // per batch of 4 slots: 0 all widths <= 5, 1 otherwise
@@ -261,21 +255,17 @@ __device__ __forceinline__ void k_batch_gen(const uint32_t* kw, const uint4* des
 
 // V-hat^T row of one dim for one tile: 16 token pairs (2u, 2u+1) -> 16 columns.
 template <int BV>
-__device__ __forceinline__ void v_vals(const uint32_t* vw, const uint8_t* sm, uint32_t lane4, uint32_t (&v)[16]) {
+__device__ __forceinline__ void v_tile(const uint32_t* vw, uint32_t taddr, const uint8_t* sm, uint32_t lane4) {
   uint32_t x[BV + 1];
 #pragma unroll
   for (int i = 0; i < BV; ++i) x[i] = vw[i * kD];
   x[BV] = 0u;
+  uint32_t v[16];
 #pragma unroll
   for (int u = 0; u < 16; ++u) {
     const int p = 2 * BV * u;
     v[u] = pair_value<BV>(x[p >> 5], x[(p >> 5) + 1], p & 31, sm, lane4);
   }
-}
-template <int BV>
-__device__ __forceinline__ void v_tile(const uint32_t* vw, uint32_t taddr, const uint8_t* sm, uint32_t lane4) {
-  uint32_t v[16];
-  v_vals<BV>(vw, sm, lane4, v);
   tc::tmem_st<16>(taddr, v);
 }
 
@@ -303,29 +293,6 @@ __device__ __forceinline__ bool named_sync_or(int id, int n, bool v) {
 }
 
 __device__ __forceinline__ void record_status(unsigned* status, unsigned code) { atomicCAS(status, 0u, code); }
-
-// Starts the copies of tiles tile0 .. tile0 + nt - 1 of one head of a paged sequence to `dst`
-// (the caller has announced their bytes on `bar`): one copy per run of tiles in one page. A
-// page outside the pool reads page 0 instead, so the announced bytes still arrive, and sets
-// *bad_page, which voids the CTA's result.
-__device__ __forceinline__ void paged_copy_tiles(uint8_t* dst, const uint8_t* pool, const PagedArgs& a,
-                                                 const int32_t* pages, int tile0, int nt, int hkv, uint64_t* bar,
-                                                 volatile int* bad_page, unsigned* status) {
-  for (int u = 0; u < nt;) {
-    const int slot = (tile0 + u) / a.page_tiles, in = tile0 + u - slot * a.page_tiles;
-    const int run = min(nt - u, a.page_tiles - in);
-    int page = __ldg(pages + slot);
-    if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages)) {
-      record_status(status, KVQ_ERR_RANGE);
-      *bad_page = 1;
-      page = 0;
-    }
-    const size_t rec = (static_cast<size_t>(page) * a.n_kv_heads + hkv) * a.page_tiles + in;
-    tc::bulk_g2s(dst + u * a.rec_bytes, pool + a.hdr_bytes + rec * a.rec_bytes,
-                 static_cast<uint32_t>(run * a.rec_bytes), bar);
-    u += run;
-  }
-}
 
 // Element i of a tensor of run-time dtype (kvq_dtype) as fp32.
 __device__ __forceinline__ float load_f32(const void* p, int dtype, int64_t i) {
@@ -363,82 +330,7 @@ struct DecArgs {
   unsigned* status;
   uint32_t wait_limit;
   int debug_no_loads;                // test hook: issue no copy, so every wait on a stage gives up
-  // paged caches
-  PagedArgs pg;
-  int slots;                         // splits of the whole batch per KV head
-  int direct;                        // a sequence of one split writes `out`, not a partial
-  void* out_rows;                    // [batch][n_q_heads][128] of out_dtype
-  int out_dtype;
-  int2* plan;                        // [batch] first split and number of splits (-1: not decoded)
 };
-
-// Element i of an output of run-time dtype.
-__device__ __forceinline__ void store_f32(void* p, int dtype, int64_t i, float v) {
-  if (dtype == KVQ_F32) static_cast<float*>(p)[i] = v;
-  else if (dtype == KVQ_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);
-  else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-}
-
-// ---------------------------------------------------------------- sharing out a ragged batch
-
-// Splits a ragged batch's chunks over a.slots CTAs per KV head. A CTA's time goes with the
-// chunks of its busiest warpgroup, so the batch is cut by the smallest p (chunks per
-// warpgroup) for which every sequence, ceil(chunks / (4 p)) splits each, fits the slots: the
-// longest sequence gets the most CTAs and no CTA more than p rounds. Each warp tries one p
-// from the lower bound (all chunks spread evenly) upwards in steps of an eighth; the last
-// warp's p leaves one split per sequence, which always fits (slots >= batch). Lengths come from
-// device memory, so a captured call follows them. Writes the CTA's share to S.job_* and, in
-// CTA 0, the plan that the merge reads. `chunks` is shared memory for a.pg.batch ints.
-__device__ __forceinline__ void share_out(const DecArgs& a, DecHeader& S, int* chunks, bool refuse) {
-  constexpr int kW = kDecThreads / 32;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = a.pg.batch;
-  const long long room = static_cast<long long>(a.pg.max_pages) * a.pg.page_tiles * kTile;
-  for (int b = tid; b < n; b += kDecThreads) {
-    const int len = __ldg(a.pg.seq_lens + b);
-    const bool ok = len >= 0 && len <= room;
-    if (!ok) record_status(a.status, KVQ_ERR_RANGE);
-    chunks[b] = ok ? (len + kChunkTokens - 1) / kChunkTokens : -1;
-  }
-  if (tid == 0) S.job_seq = -1;
-  __syncthreads();
-  int sum = 0, most = 0;
-  for (int b = lane; b < n; b += 32) {
-    sum += max(chunks[b], 0);
-    most = max(most, chunks[b]);
-  }
-  sum = __reduce_add_sync(0xffffffffu, sum);
-  most = __reduce_max_sync(0xffffffffu, most);
-  const int least = max(1, (sum + kDecWG * a.slots - 1) / (kDecWG * a.slots));
-  const int p = warp < kW - 1 ? least + (least * warp + 7) / 8 : max(1, (most + kDecWG - 1) / kDecWG);
-  int need = 0;
-  for (int b = lane; b < n; b += 32) need += (max(chunks[b], 0) + kDecWG * p - 1) / (kDecWG * p);
-  need = __reduce_add_sync(0xffffffffu, need);
-  if (lane == 0) S.job_chunks_wg[warp] = need <= a.slots ? p : 0x7fffffff;
-  __syncthreads();
-  int best = 0x7fffffff;
-  for (int w = 0; w < kW; ++w) best = min(best, S.job_chunks_wg[w]);
-  const int slot = static_cast<int>(blockIdx.x) / a.n_kv_heads;
-  int first = 0;
-  for (int b0 = 0; b0 < n; b0 += kDecThreads) {
-    const int b = b0 + tid;
-    const int c = b < n ? chunks[b] : 0;
-    const int s = (max(c, 0) + kDecWG * best - 1) / (kDecWG * best);
-    int total;
-    const int at = first + block_exclusive(s, S.scan, kW, total);
-    if (b < n) {
-      if (slot >= at && slot < at + s) {
-        S.job_seq = b;
-        S.job_len = __ldg(a.pg.seq_lens + b);
-        S.job_split = slot - at;
-        S.job_splits = s;
-      }
-      if (blockIdx.x == 0) a.plan[b] = make_int2(at, (refuse || c < 0) ? -1 : s);
-    }
-    first += total;
-  }
-  tc::fence_proxy_async_smem();      // `chunks` is a copy's destination next
-  __syncthreads();
-}
 
 // ---------------------------------------------------------------- split merge
 
@@ -524,44 +416,39 @@ __device__ __forceinline__ void split16(float x, uint32_t& hi, uint32_t& lo) {
 }
 
 // One instantiation per value mode VM: 1..8 = packed values of that width; kDenseBf16 /
-// kDenseF16 = keys-only cache with dense value rows of that type. kPaged: the cache is a
-// paged pool and the batch is ragged: a CTA takes the split that share_out gives it, finds its
-// tiles through the block table and leaves its (m, l, O) to kvq_paged_merge.
-// Threshold and scale of P': a contiguous cache keeps logits up to 2^8 above the running
-// maximum and stores P' divided by 2^8. A paged one moves the maximum at 2^3 and stores P' as
-// it is (at most 2^3 * 65504 / sqrt(128), inside fp16), so its low parts lie 2^8 further from
-// fp16's smallest values.
-template <int VM, bool kPaged = false>
+// kDenseF16 = keys-only cache with dense value rows of that type.
+template <int VM>
 __global__ void __launch_bounds__(kDecThreads, 1) kvq_decode_gtq(const DecArgs a) {
   constexpr bool kDense = VM >= kDenseBf16;
   constexpr bool kBfO = VM == kDenseBf16;                  // O operands in bf16
-  constexpr int kThr = kPaged ? 3 : kTau;                  // lazy rescale threshold
-  constexpr float kScale = kPaged ? 1.0f : static_cast<float>(1 << kTau);
-  static_assert(!(kDense && kPaged), "a pool holds its values");
   extern __shared__ __align__(1024) uint8_t sm[];
   DecHeader& S = *reinterpret_cast<DecHeader*>(sm + kHdrOff);
   uint8_t* stages = sm + decode_stage_off();
   float* rec_o = reinterpret_cast<float*>(sm + kRecOff);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int bh = blockIdx.y;
-  const int hkv = kPaged ? blockIdx.x % a.n_kv_heads : bh % a.n_kv_heads;
+  const int split = blockIdx.x, bh = blockIdx.y;
+  const int b = bh / a.n_kv_heads, hkv = bh % a.n_kv_heads;
   const int G = a.n_q_heads / a.n_kv_heads;
   const kvq_head_alloc* al = a.alloc + hkv;
-  // a paged CTA learns its sequence, length and split below, from device memory
-  int b = bh / a.n_kv_heads, split = blockIdx.x, splits = a.splits, seq_len = a.seq_len;
+  const int n_tiles = (a.seq_len + kTile - 1) / kTile;
+  const int n_chunks_all = (n_tiles + kChunkTiles - 1) / kChunkTiles;
+  const int c_begin = static_cast<int>((static_cast<long long>(split) * n_chunks_all) / a.splits);
+  const int c_end = static_cast<int>((static_cast<long long>(split + 1) * n_chunks_all) / a.splits);
+  const int n_chunks = c_end - c_begin;
+  const uint8_t* src = a.packed + a.hdr_bytes + static_cast<size_t>(bh) * a.tiles_cap * a.rec_bytes;
   const int cbytes = a.cbytes;
   const int kbytes = 4 * kD * a.bits_k;             // K words of a record
   const int NS = a.n_stages;
   const float inv_sqrt_d = 0.08838834764831845f;
   const uint32_t WL = a.wait_limit;
-  const uint8_t* src = a.packed + a.hdr_bytes + static_cast<size_t>(bh) * a.tiles_cap * a.rec_bytes;
 
   // roles: compute warps 0..15 (warpgroup g = warp / 4, quarter q = warp % 4), issuer warps 16..19
   const bool is_issuer = warp >= kDecIssuerWarp0;
   const int g = is_issuer ? warp - kDecIssuerWarp0 : warp >> 2;
   const int q = warp & 3;
   const bool issuer = is_issuer && lane == 0;
+  const int nj = (n_chunks > g) ? (n_chunks - g + kDecWG - 1) / kDecWG : 0;   // this warpgroup's chunks
   uint8_t* my_stages = stages + static_cast<size_t>(g) * NS * cbytes;
 
   // ------------------------------------------------------------------ barriers, TMEM, setup copy
@@ -584,7 +471,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_decode_gtq(const DecArgs a
     }
     tc::mbar_init(&S.setup, 1);
     S.bad = 0;
-    if constexpr (kPaged) S.bad_page = 0;
     tc::mbar_fence_init();
     tc::mbar_arrive_expect_tx(&S.setup, kLutBytes + static_cast<uint32_t>(sizeof(kvq_head_alloc)));
     tc::bulk_g2s(sm, g_dec_lut, kLutBytes, &S.setup);
@@ -597,48 +483,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_decode_gtq(const DecArgs a
   // their loads go out first, so their latency overlaps the setup below.
   const int qh = tid >> 6, qd = 2 * (tid & 63);
   float2 qin = make_float2(0.0f, 0.0f);
-  auto load_q = [&]() {
-    if (tid < 512 && qh < G) {
-      const int64_t qi = b * a.qsb + (hkv * G + qh) * a.qsh + qd;
-      qin = make_float2(load_f32(a.q, a.q_dtype, qi), load_f32(a.q, a.q_dtype, qi + 1));
-    }
-  };
-  if constexpr (!kPaged) load_q();
-  if constexpr (kPaged) {
-    if (tid == 32) {
-      unsigned code = paged_header_code(a.packed, a.pg);
-      const uint64_t dg = paged_digest(a.packed, hkv), ad = al->digest;
-      const int abk = al->bits_k, akw = al->k_words, apk = al->plan_k_cols, aps = al->plan_n_slots;
-      if (!code && !((dg == ad) & (abk == a.bits_k) & (akw == a.bits_k * kD) & (apk <= 96) & (apk >= 8) & (aps <= kPlanSlots)))
-        code = KVQ_ERR_MISMATCH;
-      if (code) {
-        S.bad = 1;
-        record_status(a.status, code);
-      }
-    }
-    __syncthreads();
-    share_out(a, S, reinterpret_cast<int*>(stages), S.bad != 0);
-    b = S.job_seq;
-    if (b < 0) {                                            // no split left for this CTA
-      if (tid == 0) tc::mbar_wait(&S.setup, 0, WL);         // its copies land before it leaves
-      tc::fence_before_sync();
-      __syncthreads();
-      tc::fence_after_sync();
-      if (warp == kDecIssuerWarp0) tc::tmem_dealloc(S.tmem_base, kTmemCols);
-      return;
-    }
-    seq_len = S.job_len;
-    split = S.job_split;
-    splits = S.job_splits;
-    load_q();
+  if (tid < 512 && qh < G) {
+    const int64_t qi = b * a.qsb + (hkv * G + qh) * a.qsh + qd;
+    qin = make_float2(load_f32(a.q, a.q_dtype, qi), load_f32(a.q, a.q_dtype, qi + 1));
   }
-  const int n_tiles = (seq_len + kTile - 1) / kTile;
-  const int n_chunks_all = (n_tiles + kChunkTiles - 1) / kChunkTiles;
-  const int c_begin = static_cast<int>((static_cast<long long>(split) * n_chunks_all) / splits);
-  const int c_end = static_cast<int>((static_cast<long long>(split + 1) * n_chunks_all) / splits);
-  const int n_chunks = c_end - c_begin;
-  const int nj = (n_chunks > g) ? (n_chunks - g + kDecWG - 1) / kDecWG : 0;   // this warpgroup's chunks
-  if (!kPaged && tid == 32) {
+  if (tid == 32) {
     // The packed header must name this layout, these widths and shapes, and this head's
     // allocation; a status left by an append is reported as is. All fields are loaded
     // before any is compared, so the loads overlap.
@@ -679,17 +528,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_decode_gtq(const DecArgs a
     uint32_t bytes = static_cast<uint32_t>(nt * a.rec_bytes);
     int rows = 0;
     if constexpr (kDense) {
-      rows = min(kChunkTokens, seq_len - ci * kChunkTokens);
+      rows = min(kChunkTokens, a.seq_len - ci * kChunkTokens);
       bytes += static_cast<uint32_t>(rows) * (2 * kD);
     }
     tc::mbar_arrive_expect_tx(&S.full[g][s], bytes);
-    if constexpr (kPaged) {
-      paged_copy_tiles(dst, a.packed, a.pg, a.pg.block_table + b * a.pg.table_stride, tile0, nt, hkv, &S.full[g][s],
-                       &S.bad_page, a.status);
-    } else {
-      tc::bulk_g2s(dst, src + static_cast<size_t>(tile0) * a.rec_bytes, static_cast<uint32_t>(nt * a.rec_bytes),
-                   &S.full[g][s]);
-    }
+    tc::bulk_g2s(dst, src + static_cast<size_t>(tile0) * a.rec_bytes, static_cast<uint32_t>(nt * a.rec_bytes),
+                 &S.full[g][s]);
     if constexpr (kDense) {
       const uint8_t* vsrc = static_cast<const uint8_t*>(a.v_dense) +
                             2 * (b * a.vsb + hkv * a.vsh + static_cast<int64_t>(ci) * kChunkTokens * a.vst);
@@ -833,9 +677,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_decode_gtq(const DecArgs a
     // l + 96; issuer warp w walks every fourth token with its own online softmax over
     // s = q . k * log2(e) / sqrt(d); the four warps then meet at a common maximum and add
     // their O shares into rec_o in a fixed order.
-    const int r_begin = static_cast<int>((static_cast<long long>(split) * a.n_recent) / splits);
-    const int r_end = static_cast<int>((static_cast<long long>(split + 1) * a.n_recent) / splits);
-    if (!kPaged && r_end > r_begin) {
+    const int r_begin = static_cast<int>((static_cast<long long>(split) * a.n_recent) / a.splits);
+    const int r_end = static_cast<int>((static_cast<long long>(split + 1) * a.n_recent) / a.splits);
+    if (r_end > r_begin) {
       const int w = g;
       float* rq = reinterpret_cast<float*>(sm + kRecQOff);  // reused: q * log2(e) / sqrt(d)
       named_sync(kDecWG + 1, 128);
@@ -951,7 +795,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_decode_gtq(const DecArgs a
       float vn = 1.0f;
       if constexpr (!kDense) vn = __half2float(__ushort_as_half(reinterpret_cast<const uint16_t*>(tq + kbytes + 2 * kTile)[lane]));
       const int tok0 = ci * kChunkTokens;
-      const bool valid = tok0 + 32 * q + lane < seq_len;
+      const bool valid = tok0 + 32 * q + lane < a.seq_len;
       // -------------------------------------------------------------- values (lane = dim)
       // V-hat^T and P' are free once the previous chunk's O products are complete
       if (j > 0 && !tc::mbar_wait(&S.ofull[g], (j - 1) & 1, WL)) *abort_flag = 1;
@@ -960,7 +804,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_decode_gtq(const DecArgs a
         // dense rows [token][128] of 16-bit values after the chunk's records; rows past the
         // sequence end are not copied and read as 0
         const uint16_t* vr = reinterpret_cast<const uint16_t*>(st + kChunkTiles * a.rec_bytes) + 32 * q + lane;
-        const int nrows = seq_len - tok0;
+        const int nrows = a.seq_len - tok0;
 #pragma unroll
         for (int u = 0; u < kChunkTiles; ++u) {
           uint32_t v[16];
@@ -1001,7 +845,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_decode_gtq(const DecArgs a
       // rescaled.
       bool over = false;
 #pragma unroll
-      for (int h = 0; h < 8; ++h) over |= sv[h] > M[h] + static_cast<float>(kThr);
+      for (int h = 0; h < 8; ++h) over |= sv[h] > M[h] + static_cast<float>(kTau);
       // a wait that gave up joins the vote, so that the warpgroup's four warps stop as one
       const bool stop = *abort_flag != 0;
       const bool any_over = named_sync_or(1 + g, 128, over || stop);
@@ -1035,7 +879,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_decode_gtq(const DecArgs a
       // -------------------------------------------------------------- P' (lane = token)
       {
         // packed values: P' = p * value norm / sqrt(d) (v-hat = norm * c / sqrt(d)); dense: p
-        const float vs = valid ? (kDense ? 1.0f : vn * inv_sqrt_d) / kScale : 0.0f;
+        const float vs = valid ? (kDense ? 1.0f : vn * inv_sqrt_d) / static_cast<float>(1 << kTau) : 0.0f;
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int h = 0; h < 8; h += 2) {
@@ -1085,10 +929,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_decode_gtq(const DecArgs a
   __syncthreads();
   allow_dependents();                                       // the next kernel may start on freed SMs
   bool aborted = bad;
-  if constexpr (kPaged) aborted |= S.bad_page != 0;
 #pragma unroll
   for (int gg = 0; gg < kDecWG; ++gg) aborted |= S.wg_abort[gg] != 0;
-  if (aborted && !bad && tid == 0) record_status(a.status, KVQ_ERR_TIMEOUT);   // keeps an earlier status
+  if (aborted && !bad && tid == 0) record_status(a.status, KVQ_ERR_TIMEOUT);
 
   // ------------------------------------------------------------------ CTA result
   // Warpgroup partials (m, l, O) combined in shared memory (the stage area is free now).
@@ -1101,7 +944,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_decode_gtq(const DecArgs a
       tc::wait_ld();
 #pragma unroll
       for (int h = 0; h < 8; ++h)
-        comb[(g * 8 + h) * kD + d] = (__uint_as_float(o[h]) + __uint_as_float(o[8 + h])) * kScale;
+        comb[(g * 8 + h) * kD + d] = (__uint_as_float(o[h]) + __uint_as_float(o[8 + h])) * static_cast<float>(1 << kTau);
     }
     const int tid_wg = 32 * q + lane;
     if (tid_wg < 8) {
@@ -1118,13 +961,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_decode_gtq(const DecArgs a
   __syncthreads();
   tc::fence_after_sync();
   if (warp == kDecIssuerWarp0) tc::tmem_dealloc(tbase, kTmemCols);
-  if (aborted) {
-    // a NaN maximum tells the merge that this share is missing
-    if (kPaged && tid < 8) a.part_m[static_cast<size_t>(blockIdx.x) * 8 + tid] = __int_as_float(0x7fc00000);
-    return;
-  }
+  if (aborted) return;
 
-  const int pitch = splits + a.n_groups;
+  const int pitch = a.splits + a.n_groups;
   float* out_bh = a.out + (static_cast<size_t>(b) * a.n_q_heads + hkv * G) * kD;
   // combine the warpgroups and the recent share: m = max, l and O = sums weighted by 2^(m_g - m)
   for (int i = tid; i < 8 * kD; i += blockDim.x) {
@@ -1135,22 +974,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_decode_gtq(const DecArgs a
     float Ls = 0.0f, Os = 0.0f;
 #pragma unroll
     for (int gg = 0; gg <= kDecWG; ++gg) {
-      if (S.wg_m[gg][h] == -INFINITY) {
-        if (kPaged && gg < kDecWG && S.wg_l[gg][h] != S.wg_l[gg][h]) Ls = S.wg_l[gg][h];   // NaN logits alone
-        continue;
-      }
+      if (S.wg_m[gg][h] == -INFINITY) continue;
       const float w = fast_exp2(S.wg_m[gg][h] - Mx);
       Ls += w * S.wg_l[gg][h];
       Os += w * (gg < kDecWG ? comb[(gg * 8 + h) * kD + d] : rec_o[h * kD + d]);
     }
-    if (splits == 1 && (!kPaged || a.direct)) {
-      if constexpr (kPaged) {
-        if (h < G) store_f32(a.out_rows, a.out_dtype, (static_cast<int64_t>(b) * a.n_q_heads + hkv * G + h) * kD + d, Os / Ls);
-      } else {
-        if (h < G) out_bh[h * kD + d] = Os / Ls;
-      }
+    if (a.splits == 1) {
+      if (h < G) out_bh[h * kD + d] = Os / Ls;
     } else {
-      const size_t e = kPaged ? static_cast<size_t>(blockIdx.x) : static_cast<size_t>(bh) * pitch + split;
+      const size_t e = static_cast<size_t>(bh) * pitch + split;
       a.part_o[(e * 8 + h) * kD + d] = Os;
       if (d == 0) {
         a.part_m[e * 8 + h] = Mx;
@@ -1158,7 +990,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_decode_gtq(const DecArgs a
       }
     }
   }
-  if (kPaged || splits == 1) return;
+  if (a.splits == 1) return;
 
   // ------------------------------------------------------------------ split merge (one or two levels)
   // The last CTA of each group of splits (ticket order) merges the group; the last group to

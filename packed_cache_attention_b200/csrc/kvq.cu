@@ -87,6 +87,9 @@ kvq_status ensure_tables() {
   static uint8_t lut[kLutBytes];
   decode_lut_image(t.centroid_f16, lut);
   { const cudaError_t e_ = cudaMemcpyToSymbol(g_dec_lut, lut, sizeof(lut)); if (e_ != cudaSuccess) return cuda_fail(e_); }
+  static uint8_t plut[kPlutBytes];
+  paged_lut_image(t.centroid_f16, plut);
+  { const cudaError_t e_ = cudaMemcpyToSymbol(g_paged_lut, plut, sizeof(plut)); if (e_ != cudaSuccess) return cuda_fail(e_); }
   static uint32_t qlut[2 * kLutEntries];
   if (!quant_lut_image(t.threshold, qlut)) return KVQ_ERR_UNSUPPORTED;
   { const cudaError_t e_ = cudaMemcpyToSymbol(g_quant_lut, qlut, sizeof(qlut)); if (e_ != cudaSuccess) return cuda_fail(e_); }
@@ -1025,21 +1028,18 @@ kvq_status launch_append_bv(const PagedArgs& a, const PagedQuant& p, const RopeA
   }
 }
 
-// Shares of a paged decode. Own pages: `slots` splits of the whole batch per KV head, one CTA
-// each; with fewer (sequence, KV head) pairs than SMs the slots fill the SMs once, else every
-// pair gets one.
-int paged_slots(int batch, int n_kv_heads) { return std::max(batch, sm_count() / n_kv_heads); }
+// CTAs per KV head of a paged decode: one CTA per SM in all (a head has one at least).
+int paged_ctas(int n_kv_heads) { return std::max(1, sm_count() / n_kv_heads); }
 
-// Prefix: query rows per CTA (kvq_prefix_gtq's R) and its pipelines.
+// Prefix: groups of kPreRows query rows per KV head, and splits of the prefix (fewer when it has
+// fewer chunks), one CTA per SM in all.
 struct PrefixPlan {
-  int rows, pipes, groups, splits;
+  int groups, splits;
 };
 PrefixPlan prefix_plan(int n_rows, int n_kv_heads) {
   PrefixPlan p;
-  p.rows = n_rows <= 32 ? 32 : n_rows <= 64 ? 64 : 128;
-  p.pipes = p.rows == 128 ? 1 : 2;
-  p.groups = (n_rows + p.rows - 1) / p.rows;
-  p.splits = std::max(1, sm_count() / (n_kv_heads * p.groups));   // fewer for a prefix of fewer chunks
+  p.groups = (n_rows + kPreRows - 1) / kPreRows;
+  p.splits = std::max(1, sm_count() / (n_kv_heads * p.groups));
   return p;
 }
 
@@ -1050,16 +1050,16 @@ struct PagedWs {
 };
 PagedWs paged_ws(int batch, int n_kv_heads, int group, bool prefix) {
   PagedWs w;
-  const size_t own = static_cast<size_t>(paged_slots(batch, n_kv_heads)) * n_kv_heads * 8;
+  const size_t own = static_cast<size_t>(4 * paged_ctas(n_kv_heads) + batch) * n_kv_heads * 8;
   size_t pre = 0;
   if (prefix) {
     const PrefixPlan p = prefix_plan(batch * group, n_kv_heads);
-    pre = static_cast<size_t>(p.splits) * n_kv_heads * p.groups * p.pipes * p.rows;
+    pre = static_cast<size_t>(p.splits) * n_kv_heads * p.groups * kPreRows;
   }
   w.plan = sizeof(WsHeader);
-  w.own_m = align_up(w.plan + sizeof(int2) * batch, 128);
+  w.own_m = align_up(w.plan + sizeof(int2) * (batch + 1), 128);
   w.own_l = align_up(w.own_m + 4 * own, 128);
-  w.own_o = align_up(w.own_l + 4 * own, 128);
+  w.own_o = align_up(w.own_l + 4 * 4 * own, 128);
   w.pre_m = align_up(w.own_o + 4 * kD * own, 128);
   w.pre_l = align_up(w.pre_m + 4 * pre, 128);
   w.pre_o = align_up(w.pre_l + 4 * pre, 128);
@@ -1067,30 +1067,32 @@ PagedWs paged_ws(int batch, int n_kv_heads, int group, bool prefix) {
   return w;
 }
 
-template <int R, int kPipes>
 kvq_status launch_prefix(PrefixArgs a, cudaStream_t s) {
   static SmemOptIn opt;
-  const int cb = chunk_bytes(a.pg.rec_bytes) * kPipes;
-  const size_t room = max_smem() - prefix_stage_off<R, kPipes>();
-  a.n_stages = static_cast<int>(std::min<size_t>(kStagesMax, room / cb));
+  const size_t cb = chunk_bytes(a.pg.rec_bytes), room = max_smem() - kPreStageOff;
+  a.n_stages = static_cast<int>(std::min<size_t>(kPgStagesMax, room / cb));
   if (a.n_stages < 1) return KVQ_ERR_UNSUPPORTED;
-  const size_t smem = prefix_stage_off<R, kPipes>() + static_cast<size_t>(a.n_stages) * cb;
-  const kvq_status st = opt.raise(kvq_prefix_gtq<R, kPipes>, smem);
+  const size_t smem = kPreStageOff + a.n_stages * cb;
+  const kvq_status st = opt.raise(kvq_prefix_gtq, smem);
   if (st != KVQ_OK) return st;
   const unsigned grid = static_cast<unsigned>(a.splits * a.row_groups * a.pg.n_kv_heads);
-  const cudaError_t e =
-      launch_pdl(kvq_prefix_gtq<R, kPipes>, dim3(grid), dim3(PrefixCfg<R, kPipes>::kThreads), smem, s, a);
+  const cudaError_t e = launch_pdl(kvq_prefix_gtq, dim3(grid), dim3(kPreThreads), smem, s, a);
   return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
 }
 
-template <int VM>
-kvq_status launch_paged_decode(const DecArgs& a, size_t smem, cudaStream_t s) {
+template <int VM, int kRows>
+kvq_status launch_paged_rows(const PagedAttn& a, size_t smem, cudaStream_t s) {
   static SmemOptIn opt;
-  const kvq_status st = opt.raise(kvq_decode_gtq<VM, true>, smem);
+  const kvq_status st = opt.raise(kvq_paged_gtq<VM, kRows>, smem);
   if (st != KVQ_OK) return st;
-  const unsigned grid = static_cast<unsigned>(a.slots * a.n_kv_heads);
-  const cudaError_t e = launch_pdl(kvq_decode_gtq<VM, true>, dim3(grid), dim3(kDecThreads), smem, s, a);
+  const unsigned grid = static_cast<unsigned>(a.ctas * a.pg.n_kv_heads);
+  const cudaError_t e = launch_pdl(kvq_paged_gtq<VM, kRows>, dim3(grid), dim3(kDecThreads), smem, s, a);
   return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
+}
+// Four rows or eight: half of the softmax is left out for groups of up to four.
+template <int VM>
+kvq_status launch_paged(const PagedAttn& a, size_t smem, cudaStream_t s) {
+  return a.group <= 4 ? launch_paged_rows<VM, 4>(a, smem, s) : launch_paged_rows<VM, 8>(a, smem, s);
 }
 
 }  // namespace
@@ -1224,9 +1226,10 @@ kvq_status kvq_paged_decode_attn(const void* q, const kvq_tensor4* qd, const voi
   const int group = qd->n_heads / d->n_kv_heads;
   const PagedWs w = paged_ws(seqs->batch, d->n_kv_heads, group, plen > 0);
   if (!ws || ws_bytes < w.total || !aligned16(ws)) return KVQ_ERR_WORKSPACE;
-  const int cb = chunk_bytes(pg.rec_bytes);
-  const size_t smem = decode_smem_bytes(cb);
-  if (smem > max_smem()) return KVQ_ERR_UNSUPPORTED;
+  const size_t cb = 4ull * chunk_bytes(pg.rec_bytes), room = max_smem() - pg_stage_off(seqs->batch);
+  const int n_stages = static_cast<int>(std::min<size_t>(kPgStagesMax, room / cb));
+  if (n_stages < 1) return KVQ_ERR_UNSUPPORTED;
+  const size_t smem = pg_stage_off(seqs->batch) + n_stages * cb;
   if ((st = ensure_tables()) != KVQ_OK) return st;
   uint8_t* w8 = static_cast<uint8_t*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1236,9 +1239,9 @@ kvq_status kvq_paged_decode_attn(const void* q, const kvq_tensor4* qd, const voi
   m.n_q_heads = qd->n_heads;
   m.n_kv_heads = d->n_kv_heads;
   m.group = group;
-  m.seq_lens = pg.seq_lens;
+  m.batch = seqs->batch;
   m.plan = reinterpret_cast<const int2*>(w8 + w.plan);
-  m.direct = plen == 0;
+  m.entries = 4 * paged_ctas(d->n_kv_heads) + seqs->batch;
   m.own_m = reinterpret_cast<const float*>(w8 + w.own_m);
   m.own_l = reinterpret_cast<const float*>(w8 + w.own_l);
   m.own_o = reinterpret_cast<const float*>(w8 + w.own_o);
@@ -1265,54 +1268,42 @@ kvq_status kvq_paged_decode_attn(const void* q, const kvq_tensor4* qd, const voi
     a.status = reinterpret_cast<unsigned*>(w8);
     a.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
     a.debug_no_loads = g_debug_no_loads.load(std::memory_order_relaxed);
-    st = pp.rows == 32 ? launch_prefix<32, 2>(a, s) : pp.rows == 64 ? launch_prefix<64, 2>(a, s) : launch_prefix<128, 1>(a, s);
-    if (st != KVQ_OK) return st;
+    if ((st = launch_prefix(a, s)) != KVQ_OK) return st;
     m.prefix_len = plen;
-    m.pre_rows = pp.rows;
     m.pre_groups = pp.groups;
     m.pre_splits = pp.splits;
-    m.pre_pipes = pp.pipes;
     m.pre_m = a.part_m;
     m.pre_l = a.part_l;
     m.pre_o = a.part_o;
   }
-  DecArgs a{};
+  PagedAttn a{};
   a.q = q;
   a.qsb = qd->stride_b;
   a.qsh = qd->stride_h;
   a.q_dtype = qd->dtype;
-  a.n_q_heads = qd->n_heads;
-  a.n_kv_heads = d->n_kv_heads;
-  a.batch = seqs->batch;
-  a.cbytes = cb;
-  a.packed = static_cast<const uint8_t*>(pool);
+  a.group = group;
+  a.pool = static_cast<const uint8_t*>(pool);
   a.alloc = static_cast<const kvq_head_alloc*>(alloc);
-  a.hdr_bytes = pg.hdr_bytes;
-  a.rec_bytes = pg.rec_bytes;
-  a.bits_k = d->bits_k;
-  a.bits_v = d->bits_v;
-  a.n_stages = decode_stages(cb);
+  a.pg = pg;
+  a.ctas = paged_ctas(d->n_kv_heads);
+  a.entries = m.entries;
+  a.n_stages = n_stages;
   a.part_m = reinterpret_cast<float*>(w8 + w.own_m);
   a.part_l = reinterpret_cast<float*>(w8 + w.own_l);
   a.part_o = reinterpret_cast<float*>(w8 + w.own_o);
+  a.plan = reinterpret_cast<int2*>(w8 + w.plan);
   a.status = reinterpret_cast<unsigned*>(w8);
   a.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
   a.debug_no_loads = g_debug_no_loads.load(std::memory_order_relaxed);
-  a.pg = pg;
-  a.slots = paged_slots(seqs->batch, d->n_kv_heads);
-  a.direct = m.direct;
-  a.out_rows = out;
-  a.out_dtype = out_dtype;
-  a.plan = reinterpret_cast<int2*>(w8 + w.plan);
   switch (d->bits_v) {
-    case 1: st = launch_paged_decode<1>(a, smem, s); break;
-    case 2: st = launch_paged_decode<2>(a, smem, s); break;
-    case 3: st = launch_paged_decode<3>(a, smem, s); break;
-    case 4: st = launch_paged_decode<4>(a, smem, s); break;
-    case 5: st = launch_paged_decode<5>(a, smem, s); break;
-    case 6: st = launch_paged_decode<6>(a, smem, s); break;
-    case 7: st = launch_paged_decode<7>(a, smem, s); break;
-    default: st = launch_paged_decode<8>(a, smem, s); break;
+    case 1: st = launch_paged<1>(a, smem, s); break;
+    case 2: st = launch_paged<2>(a, smem, s); break;
+    case 3: st = launch_paged<3>(a, smem, s); break;
+    case 4: st = launch_paged<4>(a, smem, s); break;
+    case 5: st = launch_paged<5>(a, smem, s); break;
+    case 6: st = launch_paged<6>(a, smem, s); break;
+    case 7: st = launch_paged<7>(a, smem, s); break;
+    default: st = launch_paged<8>(a, smem, s); break;
   }
   if (st != KVQ_OK) return st;
   const cudaError_t e = launch_pdl(kvq_paged_merge, dim3(static_cast<unsigned>(seqs->batch * qd->n_heads)),
