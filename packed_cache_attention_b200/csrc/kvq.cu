@@ -1028,7 +1028,7 @@ kvq_status launch_append_bv(const PagedArgs& a, const PagedQuant& p, const RopeA
   }
 }
 
-// CTAs per KV head of a paged decode: one CTA per SM in all (a head has one at least).
+// CTAs per KV head of a paged decode: one per SM in all (a head has one at least).
 int paged_ctas(int n_kv_heads) { return std::max(1, sm_count() / n_kv_heads); }
 
 // Prefix: groups of kPreRows query rows per KV head, and splits of the prefix (fewer when it has

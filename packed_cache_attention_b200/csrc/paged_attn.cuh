@@ -15,8 +15,8 @@
 // the SMs. One CTA per (sequence, head) instead took 217 us on 32 sequences of 64 to 16384 tokens, where
 // the longest sequence set the time.
 //
-// Inside a warpgroup: K-hat's 96 columns of tensor memory hold V-hat^T next (128 columns per
-// warpgroup in all), the issuing warp copies a chunk's keys and values separately, so the keys of
+// Inside a warpgroup: 64 of K-hat's 96 columns of tensor memory hold V-hat^T next (128 columns per
+// warpgroup in all); the next chunk's first 32 columns are looked up while O's products run. The issuing warp copies a chunk's keys and values separately, so the keys of
 // the next chunk arrive while the values of this one are used, even with a single buffer of each.
 // Every wait is bounded; a warpgroup that gave up, and a segment with a page outside the pool,
 // leave NaN maxima, at which the merge leaves the rows as they are.
@@ -28,6 +28,7 @@
 namespace kvq {
 
 constexpr int kPgStagesMax = 4;
+constexpr int kPgVCol = 32;               // first of V-hat^T's 64 columns; K-hat has columns 0..95
 
 struct PagedAttn {
   const void* q;
@@ -57,12 +58,11 @@ struct PgHeader {
   int bad;
   int wg_abort[4], wg_stop[4];
   int stage_bad[4][kPgStagesMax];          // the chunk of this stage lies in a page outside the pool
-  int n_slots, k_cols;
+  int k_cols;
   alignas(16) float qscale[4][8];
   float xch[4][4][8];
   int scan[kDecThreads / 32];
-  alignas(16) uint4 kdesc[kPlanSlots];
-  int wide[kPlanSlots / 4];
+  KSlots slots;
   alignas(16) float dequant[kH];
   alignas(4) int8_t col_of[kH];            // column of a block (-1: width 0)
 };
@@ -75,6 +75,18 @@ constexpr int kPgPOff = kPgQOff + 4 * kPgQBytes;
 constexpr int kPgHdrOff = kPgPOff + 4 * kPgPBytes;
 constexpr int kPgScanOff = kPgHdrOff + (static_cast<int>(sizeof(PgHeader)) + 15) / 16 * 16;
 __host__ __device__ constexpr int pg_stage_off(int batch) { return (kPgScanOff + 4 * (batch + 1) + 127) / 128 * 128; }
+
+// Place in a ring of stages and the parity of its phase.
+struct Ring {
+  int s = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++s == n) {
+      s = 0;
+      parity ^= 1u;
+    }
+  }
+};
 
 // The 4 * ctas warpgroups of a head share `chunks` chunks: as few as keep the longest range.
 __device__ __forceinline__ int pg_workers(int chunks, int ctas) {
@@ -165,18 +177,17 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
   if (tid < kH) S.col_of[tid] = -1;
   __syncthreads();
   grid_dependency_wait();
-  // ------------------------------------------------------------------ header, descriptors, the batch
-  if (tid < kPlanSlots) {
-    bool bad;
-    S.kdesc[tid] = k_slot_desc(al->plan_slot[tid], kD * a.pg.bits_k, bad);
-    if (bad) {
-      S.bad = 1;
-      record_status(a.status, KVQ_ERR_MISMATCH);
+  // ------------------------------------------------------------------ header, slots, the batch
+  if (warp == 0) {
+    const int k_cols = min(max(al->plan_k_cols, 8), 96) & ~7;
+    const bool ok = k_slots(al->plan_slot, k_cols, kD * a.pg.bits_k, S.slots);
+    if (lane == 0) {
+      S.k_cols = k_cols;
+      if (!ok) {
+        S.bad = 1;
+        record_status(a.status, KVQ_ERR_MISMATCH);
+      }
     }
-  } else if (tid >= 32 && tid < 32 + kPlanSlots / 4) {
-    uint32_t wmax = 0;
-    for (int i = 0; i < 4; ++i) wmax = max(wmax, al->plan_slot[4 * (tid - 32) + i] & 15u);
-    S.wide[tid - 32] = wmax > 5;
   } else if (tid >= 64 && tid < 64 + 96) {
     const int c = tid - 64, blk = al->plan_col_block[c];
     if (blk >= 0 && blk < kH && c < al->plan_k_cols) S.col_of[blk] = static_cast<int8_t>(c);
@@ -193,8 +204,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
       S.bad = 1;
       record_status(a.status, code);
     }
-    S.n_slots = min(max(aps, 1), kPlanSlots);
-    S.k_cols = min(max(apk, 8), 96);
   }
   __syncthreads();
   const int chunks = pg_scan(a, S, cs, S.bad != 0);
@@ -243,9 +252,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
       ck.nt = cv.nt = tiles_of(b0);
     }
     int nk = 0, nv = 0;                                     // chunks whose K (V) copies are started
+    Ring rk, rv;
     auto copy_k = [&]() {
       const int tile = ck.c * kChunkTiles + lane;
-      const int nt = min(kChunkTiles, ck.nt - ck.c * kChunkTiles), s = nk % NS;
+      const int nt = min(kChunkTiles, ck.nt - ck.c * kChunkTiles), s = rk.s;
       bool off = false;
       const uint8_t* rec = nullptr;
       if (lane < nt) rec = paged_record(a.pool, a.pg, a.pg.block_table + ck.b * a.pg.table_stride, tile, hkv, off);
@@ -258,11 +268,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
       __syncwarp();
       if (lane < nt) tc::bulk_g2s(my_stages + static_cast<size_t>(s) * cbytes + lane * kbytes, rec, kbytes, &S.fullk[g][s]);
       ++nk;
+      rk.next(NS);
       if (nk < total) advance(ck);
     };
     auto copy_v = [&]() {
       const int tile = cv.c * kChunkTiles + lane;
-      const int nt = min(kChunkTiles, cv.nt - cv.c * kChunkTiles), s = nv % NS;
+      const int nt = min(kChunkTiles, cv.nt - cv.c * kChunkTiles), s = rv.s;
       bool off = false;
       const uint8_t* rec = nullptr;
       if (lane < nt) rec = paged_record(a.pool, a.pg, a.pg.block_table + cv.b * a.pg.table_stride, tile, hkv, off);
@@ -272,6 +283,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
         tc::bulk_g2s(my_stages + static_cast<size_t>(s) * cbytes + kChunkTiles * kbytes + lane * vbytes, rec + kbytes, vbytes,
                      &S.fullv[g][s]);
       ++nv;
+      rv.next(NS);
       if (nv < total) advance(cv);
     };
     const bool loads = !a.debug_no_loads;
@@ -313,7 +325,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
       if (lane == 0) {
 #pragma unroll
         for (int ks = 0; ks < kChunkTokens / 16; ++ks)
-          tc::mma_ts(tO, tbase + 8 * ks, tc::sdesc(bp + 512 * ks, 256, 128), id_o, (!fresh || ks > 0) ? 1u : 0u);
+          tc::mma_ts(tO, tbase + kPgVCol + 8 * ks, tc::sdesc(bp + 512 * ks, 256, 128), id_o, (!fresh || ks > 0) ? 1u : 0u);
         tc::mma_commit(&S.ofull[g]);
       }
       __syncwarp();
@@ -336,13 +348,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
     const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
     const uint32_t lane4 = static_cast<uint32_t>(lane) << 2;
     const int t = 32 * q + lane;                            // token of a chunk, dim of a value, thread of the warpgroup
-    const int nb = (S.n_slots + 3) >> 2;
     uint8_t* pb = sm + kPgPOff + g * kPgPBytes + (t >> 3) * 256 + (t & 7) * 16;
     uint8_t* qb = sm + kPgQOff + g * kPgQBytes;
     const float* qs = S.qscale[g];
     if (x1 > x0 && !tc::mbar_wait(&S.setup, 0, WL)) *abort_flag = 1;
 
     int j = 0;                                              // chunks done
+    Ring ring;
     int x = x0, b = b0;
     bool stopped = false;
     while (x < x1) {
@@ -400,29 +412,26 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
       }
       int seg_bad = 0;
       for (int i = 0; i < nseg; ++i, ++j) {
-        const int s = j % NS;
+        const int s = ring.s;
         const uint8_t* st = my_stages + static_cast<size_t>(s) * cbytes;
         // ------------------------------------------------------------ keys (lane = token)
-        if (!tc::mbar_wait(&S.fullk[g][s], (j / NS) & 1, WL)) *abort_flag = 1;
+        if (!tc::mbar_wait(&S.fullk[g][s], ring.parity, WL)) *abort_flag = 1;
         seg_bad |= *reinterpret_cast<volatile int*>(&S.stage_bad[g][s]);
         const uint8_t* kw = st + q * kbytes + lane4;
-        for (int bt = 0; bt < nb; ++bt) {
-          uint32_t v16[16];
-          if (S.wide[bt]) k_vals<true>(kw, S.kdesc + 4 * bt, sm, lane4, v16);
-          else k_vals<false>(kw, S.kdesc + 4 * bt, sm, lane4, v16);
-          if (bt == 0 && j > 0) {                           // the buffer held the last chunk's V-hat^T
-            if (!tc::mbar_wait(&S.ofull[g], (j - 1) & 1, WL)) *abort_flag = 1;
-            tc::fence_after_sync();
-          }
-          tc::tmem_st<16>(tbase + lane_base + 16 * bt, v16);
-        }
+        auto put = [&](int slot, const uint32_t (&v)[4]) { tc::tmem_st<4>(tbase + lane_base + 4 * slot, v); };
+        // the first columns are free already, the others held the last chunk's V-hat^T
+        k_lookup(kw, S.slots, 0, kPgVCol / 4, sm, lane4, put);
+        if (j > 0 && !tc::mbar_wait(&S.ofull[g], (j - 1) & 1, WL)) *abort_flag = 1;
+        tc::fence_after_sync();
+        k_lookup(kw, S.slots, kPgVCol / 4, kPlanSlots, sm, lane4, put);
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&S.kready[g]);
         // ------------------------------------------------------------ values (lane = dim)
         const uint8_t* sv = st + kChunkTiles * kbytes;
-        if (!tc::mbar_wait(&S.fullv[g][s], (j / NS) & 1, WL)) *abort_flag = 1;
+        if (!tc::mbar_wait(&S.fullv[g][s], ring.parity, WL)) *abort_flag = 1;
+        ring.next(NS);
         const bool valid = (c_first + i) * kChunkTokens + t < len;
         const uint16_t* nrm = reinterpret_cast<const uint16_t*>(sv + q * vbytes) + lane;
         const float kn = valid ? __half2float(__ushort_as_half(nrm[0])) : 0.0f;
@@ -433,12 +442,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
           v_vals<VM>(vw, sm, lane4, v16);
           if (!tc::mbar_wait(&S.sfull[g], j & 1, WL)) *abort_flag = 1;   // K-hat is read
           tc::fence_after_sync();
-          tc::tmem_st<16>(tbase + lane_base, v16);
+          tc::tmem_st<16>(tbase + kPgVCol + lane_base, v16);
 #pragma unroll
           for (int u = 1; u < kChunkTiles; ++u) {
             vw = reinterpret_cast<const uint32_t*>(sv + u * vbytes + 4 * kTile) + t;
             v_vals<VM>(vw, sm, lane4, v16);
-            tc::tmem_st<16>(tbase + lane_base + 16 * u, v16);
+            tc::tmem_st<16>(tbase + kPgVCol + lane_base + 16 * u, v16);
           }
         }
         // ------------------------------------------------------------ logits minus the maxima
@@ -588,11 +597,11 @@ struct MergeArgs {
 
 constexpr int kPreRows = 128;              // query rows of a CTA on the prefix
 
-constexpr int kMergeWarps = 8;
+constexpr int kMergeWarps = 16;
 
 // One CTA joins the shares of one (sequence, query head): the prefix's splits, then the
-// sequence's own. Warp w folds shares w, w + 8, .. with its own running maximum (lane = 4 dims,
-// the loads of four shares in flight), then the warps meet in shared memory. The order of the
+// sequence's own. Warp w folds shares w, w + 16, .. with its own running maximum (lane = 4 dims,
+// the loads of eight shares in flight), then the warps meet in shared memory. The order of the
 // sums is fixed. A NaN maximum marks a missing share: the row is left as it is.
 __global__ void __launch_bounds__(kMergeWarps * 32) kvq_paged_merge(const MergeArgs a) {
   __shared__ float sm_m[kMergeWarps], sm_l[kMergeWarps];
@@ -614,7 +623,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kvq_paged_merge(const MergeA
   float M = -INFINITY, L = 0.0f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   bool missing = false;
-  constexpr int kBatch = 4;
+  constexpr int kBatch = 8;
   for (int i0 = warp; i0 < n; i0 += kMergeWarps * kBatch) {
     float mv[kBatch], lv[kBatch];
     float4 ov[kBatch];

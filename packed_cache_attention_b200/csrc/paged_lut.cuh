@@ -4,9 +4,9 @@
 // A lookup turns the 2w bits of two consecutive codes into one word of two fp16 centroids. For
 // widths 1..4 every lane has its own copy of the table (entry i of lane l at word 32 i + l), so
 // 32 lanes never share a bank; with one shared copy of width 4's 256 entries a warp's lookup
-// takes 3.5 passes on average. A field is moved to bit 7 of a word by one funnel shift, masked and
-// joined with the lane and the table's base by one three-input operation, and is then the
-// entry's byte address: three instructions a pair. Width 5 (4 KB) has one copy, its fields at bit 2;
+// takes 3.5 passes on average. A field is moved to bit 7 of a word by one shift, masked and joined
+// with the lane by one three-input operation, and is then the entry's byte offset: three
+// instructions a pair, two of them on the half-rate integer pipe. Width 5 (4 KB) has one copy, its fields at bit 2;
 // widths 6..8 (the few blocks of the highest energy, or large budgets) take two single lookups.
 #pragma once
 
@@ -15,12 +15,11 @@
 
 namespace kvq {
 
-// Byte offsets of the tables (pair tables: a multiple of their size, so that OR adds them).
+// Byte offsets of the tables.
 __host__ __device__ constexpr int plut_off(int w) {
   return w == 4 ? 0 : w == 3 ? 32768 : w == 2 ? 40960 : w == 1 ? 43008 : w == 6 ? 43520 : w == 7 ? 43648 : w == 8 ? 44032 : 45056;
 }
 constexpr int kPlutBytes = 49152;
-__host__ __device__ constexpr int plut_pos(int w) { return w <= 4 ? 7 : 2; }   // bit position of a field
 
 // Host: the image from the fp16 centroid table (width w at c16 + 2^w - 2).
 inline void paged_lut_image(const uint16_t* c16, uint8_t* img) {
@@ -43,72 +42,40 @@ __device__ __align__(16) uint8_t g_paged_lut[kPlutBytes];
 
 // ---------------------------------------------------------------- keys
 
-// Descriptor of a plan slot (4 block pairs of one width), read by every lane:
-//   x  byte offset of the first stream word of the lane's token (-128 when the field's place
-//      reaches back before the stream: what is read there is masked out)
-//   y  shift that brings the first code to its place, then 2w, 4w, 6w, one per byte
-//   z  mask of a pair in its place (0: a wide slot)
-//   w  table base, bit 31 set when the table has a copy per lane; a wide slot: its width
-__device__ __forceinline__ uint4 k_slot_desc(uint32_t e, int stream_bits, bool& bad) {
+// Descriptor of a plan slot (4 block pairs of one width), read by every lane. A narrow slot
+// (width <= 5): `a` = byte offset of the stream word where the first field's place starts (-128 when
+// it reaches back before the stream: what is read there is masked out), shift that brings the
+// field to its place, 2w, mask of a field in its place; `b` = table base, lane bits of an address.
+// A wide slot: offset, shift and width of the first code.
+struct KSlots {
+  alignas(16) uint4 a[kPlanSlots];
+  alignas(8) uint2 b[kPlanSlots];
+  int n_wide, n;                          // widths descend: slots 0 .. n_wide - 1 are wide
+};
+
+// Builds the descriptors of `n_cols` columns (a multiple of 8; slots past the plan's last are empty:
+// finite values against zero rows of Q'). False for a slot that starts past the stream or a
+// wide one behind a narrow one. A whole warp, lane = slot.
+__device__ __forceinline__ bool k_slots(const uint32_t* slots, int n_cols, int stream_bits, KSlots& S) {
+  const int s = threadIdx.x & 31, n = n_cols / 4;
+  const uint32_t e = s < n ? slots[s] : 0u;
   uint32_t w = e & 15u, off = e >> 8;
-  bad = w > 8 || (w > 0 && off >= static_cast<uint32_t>(stream_bits));
-  if (bad || w == 0) { w = 1; off = 0; }               // an empty slot: finite values against zero rows of Q'
-  const int pos = w <= 5 ? plut_pos(static_cast<int>(w)) : 0;
-  const int at = static_cast<int>(off) - pos;
-  uint4 d;
-  d.x = static_cast<uint32_t>((at >> 5) * 128);
-  d.y = (static_cast<uint32_t>(at) & 31u) | (2 * w) << 8 | (4 * w) << 16 | (6 * w) << 24;
-  d.z = w <= 5 ? ((1u << (2 * w)) - 1u) << pos : 0u;
-  d.w = w <= 5 ? static_cast<uint32_t>(plut_off(static_cast<int>(w))) | (w <= 4 ? 0x80000000u : 0u) : w;
-  return d;
-}
-
-// One wide slot (widths 6..8) from its two aligned stream words.
-__device__ __forceinline__ void k_wide_vals(uint32_t w, uint32_t r0, uint32_t r1, const uint8_t* lut, uint32_t* v) {
-  const uint8_t* t = lut + (w == 6 ? plut_off(6) : w == 7 ? plut_off(7) : plut_off(8));
-  const uint32_t m = (2u << w) - 2u;                   // a code, doubled
-  uint64_t r = (static_cast<uint64_t>(r1) << 32 | r0) << 1;
-  const uint32_t top = r1 >> 31;                       // the bit that the doubling pushed out
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t a = static_cast<uint32_t>(r) & m;
-    r >>= w;
-    if (k == 0) r |= static_cast<uint64_t>(top) << (64 - w);
-    const uint32_t b = static_cast<uint32_t>(r) & m;
-    r >>= w;
-    v[k] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(t + a)) |
-           static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(t + b)) << 16;
+  bool ok = w <= 8 && (w == 0 || off < static_cast<uint32_t>(stream_bits));
+  if (!ok || w == 0) { w = 1; off = 0; }
+  const uint32_t wide = __ballot_sync(0xffffffffu, w > 5);
+  const int n_wide = __popc(wide);
+  ok = ok && wide == (1u << n_wide) - 1u;
+  const int at = static_cast<int>(off) - (w <= 4 ? 7 : w == 5 ? 2 : 0);
+  if (s < n) {
+    S.a[s] = make_uint4(static_cast<uint32_t>((at >> 5) * 128), static_cast<uint32_t>(at) & 31u, w <= 5 ? 2 * w : w,
+                        w <= 5 ? ((1u << (2 * w)) - 1u) << (w <= 4 ? 7 : 2) : 0u);
+    S.b[s] = make_uint2(static_cast<uint32_t>(plut_off(static_cast<int>(w))), w <= 4 ? 0x7cu : 0u);
   }
-}
-
-// 16 K-hat columns (4 plan slots) of this lane's token; kw points at word 0 of the token (word i
-// at byte 128 i). kWide: some slot of the four is wider than 5.
-template <bool kWide>
-__device__ __forceinline__ void k_vals(const uint8_t* kw, const uint4* desc, const uint8_t* lut, uint32_t lane4,
-                                       uint32_t (&v)[16]) {
-  uint4 d[4];
-  uint32_t r0[4], r1[4], lb[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    d[i] = desc[i];
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(kw + static_cast<int>(d[i].x));
-    const uint32_t x0 = p[0], x1 = p[32], x2 = p[64];
-    r0[i] = __funnelshift_r(x0, x1, d[i].y);
-    r1[i] = __funnelshift_r(x1, x2, d[i].y);
-    lb[i] = (d[i].w & 0xffffu) | (static_cast<int>(d[i].w) < 0 ? lane4 : 0u);
+  if (s == 0) {
+    S.n_wide = n_wide;
+    S.n = n;
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (kWide && d[i].z == 0u) {
-      k_wide_vals(d[i].w, r0[i], r1[i], lut, v + 4 * i);
-      continue;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t t = (k == 0) ? r0[i] : __funnelshift_r(r0[i], r1[i], d[i].y >> (8 * k));
-      v[4 * i + k] = *reinterpret_cast<const uint32_t*>(lut + ((t & d[i].z) | lb[i]));
-    }
-  }
+  return __all_sync(0xffffffffu, ok);
 }
 
 // ---------------------------------------------------------------- values
@@ -137,6 +104,62 @@ __device__ __forceinline__ void v_vals(const uint32_t* vw, const uint8_t* lut, u
   for (int u = 0; u < 16; ++u) {
     const int p = 2 * BV * u;
     v[u] = pair_of<BV>(x[p >> 5], x[(p >> 5) + 1], p & 31, lut, lane4);
+  }
+}
+
+// The 4 words of one wide slot from its two aligned stream words.
+template <int W>
+__device__ __forceinline__ void k_wide_vals(uint32_t r0, uint32_t r1, const uint8_t* lut, uint32_t (&v)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int p = 2 * W * k;
+    v[k] = p < 32 ? pair_of<W>(r0, r1, p, lut, 0u) : pair_of<W>(r1, 0u, p - 32, lut, 0u);
+  }
+}
+
+// K-hat columns of slots first .. end - 1 (at most S.n) of the lane's token; kw: its word 0 (word i at
+// byte 128 i). put(slot, v) takes a slot's 4 columns. Narrow slots of every width go through one
+// sequence of instructions, two at a time. Words past the stream are read inside the stage and not
+// used.
+template <typename Put>
+__device__ __forceinline__ void k_lookup(const uint8_t* kw, const KSlots& S, int first, int end, const uint8_t* lut,
+                                         uint32_t lane4, Put put) {
+  end = min(end, S.n);
+  const int wide_end = min(end, S.n_wide);
+  int s = first;
+#pragma unroll 1
+  for (; s < wide_end; ++s) {
+    const uint4 d = S.a[s];
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(kw + static_cast<int>(d.x));
+    const uint32_t x0 = p[0], x1 = p[32], x2 = p[64];
+    const uint32_t r0 = __funnelshift_r(x0, x1, d.y), r1 = __funnelshift_r(x1, x2, d.y);
+    uint32_t v[4];
+    if (d.z == 6) k_wide_vals<6>(r0, r1, lut, v);
+    else if (d.z == 7) k_wide_vals<7>(r0, r1, lut, v);
+    else k_wide_vals<8>(r0, r1, lut, v);
+    put(s, v);
+  }
+#pragma unroll 1
+  for (; s < end; s += 2) {
+    // (an odd number of slots: the last is looked up twice)
+    const int k1 = min(s + 1, end - 1);
+    const uint4 d[2] = {S.a[s], S.a[k1]};
+    const uint2 b[2] = {S.b[s], S.b[k1]};
+    uint32_t v[2][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(kw + static_cast<int>(d[u].x));
+      const uint32_t x0 = p[0], x1 = p[32], x2 = p[64];
+      const uint32_t r0 = __funnelshift_r(x0, x1, d[u].y), r1 = __funnelshift_r(x1, x2, d[u].y);
+      const uint32_t lb = b[u].x | (lane4 & b[u].y);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t f = (k == 0) ? r0 : __funnelshift_r(r0, r1, d[u].z * k);
+        v[u][k] = *reinterpret_cast<const uint32_t*>(lut + ((f & d[u].w) | lb));
+      }
+    }
+    put(s, v[0]);
+    put(k1, v[1]);
   }
 }
 

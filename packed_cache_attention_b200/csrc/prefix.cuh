@@ -54,7 +54,7 @@ struct PreHeader {
   uint32_t tmem_base;
   int bad, bad_page, abort;
   int k_cols;
-  alignas(16) uint4 kdesc[kPlanSlots];
+  KSlots slots;
   alignas(16) float dequant[kH];
   int8_t col_block[96];
   alignas(16) float norm[2][2][kChunkTokens];   // [chunk parity][key, value / sqrt(d)][token]
@@ -123,12 +123,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
   if (is_issuer) tc::tmem_alloc(&S.tmem_base, kTmemCols);
   __syncthreads();
   grid_dependency_wait();
-  if (tid < kPlanSlots) {
-    bool off;
-    S.kdesc[tid] = k_slot_desc(al->plan_slot[tid], kD * a.pg.bits_k, off);
-    if (off) {
-      S.bad = 1;
-      record_status(a.status, KVQ_ERR_MISMATCH);
+  if (warp == 0) {
+    const int k_cols = min(max(al->plan_k_cols, 8), 96) & ~7;
+    const bool ok = k_slots(al->plan_slot, k_cols, kD * a.pg.bits_k, S.slots);
+    if (lane == 0) {
+      S.k_cols = k_cols;
+      if (!ok) {
+        S.bad = 1;
+        record_status(a.status, KVQ_ERR_MISMATCH);
+      }
     }
   } else if (tid >= 64 && tid < 64 + 96) {
     const int blk = al->plan_col_block[tid - 64];
@@ -146,7 +149,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
       S.bad = 1;
       record_status(a.status, code);
     }
-    S.k_cols = min(max(apk, 8), 96) & ~7;
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -169,8 +171,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
     // ------------------------------------------------------------------ issuing warp
     // Lane 0 issues the products; lanes 0..3 each copy one tile of a chunk.
     int nk = 0, nv = 0;                                     // chunks whose K (V) copies are started
-    auto copy_part = [&](int& i, uint64_t* bars, int skip, int bytes, int at) {
-      const int s = i % NS, tile0 = (c_begin + i) * kChunkTiles;
+    Ring rk, rv;
+    auto copy_part = [&](int& i, Ring& r, uint64_t* bars, int skip, int bytes, int at) {
+      const int s = r.s, tile0 = (c_begin + i) * kChunkTiles;
       const int nt = min(kChunkTiles, n_tiles - tile0);
       bool off = false;
       const uint8_t* rec = nullptr;
@@ -184,9 +187,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
       if (lane < nt)
         tc::bulk_g2s(stages + static_cast<size_t>(s) * cbytes + at + lane * bytes, rec + skip, bytes, &bars[s]);
       ++i;
+      r.next(NS);
     };
-    auto copy_k = [&]() { copy_part(nk, S.fullk, 0, kbytes, 0); };
-    auto copy_v = [&]() { copy_part(nv, S.fullv, kbytes, vbytes, kChunkTiles * kbytes); };
+    auto copy_k = [&]() { copy_part(nk, rk, S.fullk, 0, kbytes, 0); };
+    auto copy_v = [&]() { copy_part(nv, rv, S.fullv, kbytes, vbytes, kChunkTiles * kbytes); };
     const bool loads = !a.debug_no_loads;
     if (loads)
       while (nv < min(NS, n)) {
@@ -302,30 +306,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
     named_sync(1, 512);                                     // the staged rows are read
     if (!tc::mbar_wait(&S.setup, 0, WL)) *abort_flag = 1;
 
-    // Khat(j) and the norms of its tokens (lane = token; a warpgroup takes every fourth slot)
+    // Khat(j) and the norms of its tokens (lane = token; a warpgroup takes a quarter of the slots)
+    Ring rk, rv;
     auto keys = [&](int j) {
-      const int s = j % NS;
-      if (!tc::mbar_wait(&S.fullk[s], (j / NS) & 1, WL)) *abort_flag = 1;
+      const int s = rk.s;
+      if (!tc::mbar_wait(&S.fullk[s], rk.parity, WL)) *abort_flag = 1;
+      rk.next(NS);
       const uint8_t* rec = stages + static_cast<size_t>(s) * cbytes + q * kbytes;
       const uint8_t* kw = rec + lane4;
-      for (int sl = wg; sl < 2 * k_steps; sl += 4) {
-        const uint4 d = S.kdesc[sl];
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(kw + static_cast<int>(d.x));
-        const uint32_t x0 = p[0], x1 = p[32], x2 = p[64];
-        const uint32_t r0 = __funnelshift_r(x0, x1, d.y), r1 = __funnelshift_r(x1, x2, d.y);
-        uint32_t v[4];
-        if (d.z == 0u) {
-          k_wide_vals(d.w, r0, r1, sm, v);
-        } else {
-          const uint32_t lb = (d.w & 0xffffu) | (static_cast<int>(d.w) < 0 ? lane4 : 0u);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t x = (k == 0) ? r0 : __funnelshift_r(r0, r1, d.y >> (8 * k));
-            v[k] = *reinterpret_cast<const uint32_t*>(sm + ((x & d.z) | lb));
-          }
-        }
-        *reinterpret_cast<uint4*>(sm + kPreKOff + sl * 2048 + t * 16) = make_uint4(v[0], v[1], v[2], v[3]);
-      }
+      k_lookup(kw, S.slots, S.slots.n * wg / 4, S.slots.n * (wg + 1) / 4, sm, lane4, [&](int slot, const uint32_t (&v)[4]) {
+        *reinterpret_cast<uint4*>(sm + kPreKOff + slot * 2048 + t * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+      });
       if (wg == (j & 3)) {
         const bool valid = (c_begin + j) * kChunkTokens + t < a.len;
         const uint16_t* nrm = reinterpret_cast<const uint16_t*>(rec + 4 * kD * a.pg.bits_k) + lane;
@@ -342,7 +333,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
     const uint32_t tO = tb + kPreO + lane_base + 32 * wg;
     bool stopped = false;
     for (int j = 0; j < n; ++j) {
-      const int s = j % NS;
       if (!tc::mbar_wait(&S.sfull, j & 1, WL)) *abort_flag = 1;
       tc::fence_after_sync();
       if (j + 1 < n) keys(j + 1);
@@ -434,7 +424,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
         tc::tmem_st<16>(tS + 16, lo);
       }
       // ------------------------------------------------------------ values (lane = dim, one tile a warpgroup)
-      if (!tc::mbar_wait(&S.fullv[s], (j / NS) & 1, WL)) *abort_flag = 1;
+      const int s = rv.s;
+      if (!tc::mbar_wait(&S.fullv[s], rv.parity, WL)) *abort_flag = 1;
+      rv.next(NS);
       uint32_t v16[16];
       v_vals_any(a.pg.bits_v,
                  reinterpret_cast<const uint32_t*>(stages + static_cast<size_t>(s) * cbytes + kChunkTiles * kbytes + wg * vbytes) + t,
