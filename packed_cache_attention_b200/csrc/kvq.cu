@@ -1241,7 +1241,8 @@ kvq_status kvq_paged_decode_attn(const void* q, const kvq_tensor4* qd, const voi
   m.group = group;
   m.batch = seqs->batch;
   m.plan = reinterpret_cast<const int2*>(w8 + w.plan);
-  m.entries = 4 * paged_ctas(d->n_kv_heads) + seqs->batch;
+  m.ctas = paged_ctas(d->n_kv_heads);
+  m.entries = 4 * m.ctas + seqs->batch;
   m.own_m = reinterpret_cast<const float*>(w8 + w.own_m);
   m.own_l = reinterpret_cast<const float*>(w8 + w.own_l);
   m.own_o = reinterpret_cast<const float*>(w8 + w.own_o);
@@ -1262,6 +1263,7 @@ kvq_status kvq_paged_decode_attn(const void* q, const kvq_tensor4* qd, const voi
     a.len = plen;
     a.splits = pp.splits;
     a.row_groups = pp.groups;
+    a.low_p = out_dtype != KVQ_BF16;
     a.part_m = reinterpret_cast<float*>(w8 + w.pre_m);
     a.part_l = reinterpret_cast<float*>(w8 + w.pre_l);
     a.part_o = reinterpret_cast<float*>(w8 + w.pre_o);
@@ -1306,8 +1308,9 @@ kvq_status kvq_paged_decode_attn(const void* q, const kvq_tensor4* qd, const voi
     default: st = launch_paged<8>(a, smem, s); break;
   }
   if (st != KVQ_OK) return st;
-  const cudaError_t e = launch_pdl(kvq_paged_merge, dim3(static_cast<unsigned>(seqs->batch * qd->n_heads)),
-                                   dim3(kMergeWarps * 32), 0, s, m);
+  const int rows = seqs->batch * qd->n_heads;
+  const cudaError_t e = launch_pdl(kvq_paged_merge, dim3(static_cast<unsigned>(rows)),
+                                   dim3((rows <= 2 * sm_count() ? kMergeWarps : 4) * 32), 0, s, m);
   return e == cudaSuccess ? launch_status() : cuda_fail(e);
 }
 

@@ -12,7 +12,7 @@
 // sequences of its range, building Q' anew for each, and leaves one (m, l, O) per sequence it
 // met. Warpgroup w of the list and sequence b share entry w + b: along the list either w or b grows,
 // so no two pairs meet. The fewest warpgroups that keep the longest range are used, spread over
-// the SMs. One CTA per (sequence, head) instead took 217 us on 32 sequences of 64 to 16384 tokens, where
+// the SMs; those of a CTA that all lie in one sequence join their results first. One CTA per (sequence, head) instead took 217 us on 32 sequences of 64 to 16384 tokens, where
 // the longest sequence set the time.
 //
 // Inside a warpgroup: 64 of K-hat's 96 columns of tensor memory hold V-hat^T next (128 columns per
@@ -61,6 +61,7 @@ struct PgHeader {
   int k_cols;
   alignas(16) float qscale[4][8];
   float xch[4][4][8];
+  float join_m[4][8], join_l[4][4][8];     // shares of one sequence: [warpgroup][row], [warpgroup][quarter][row]
   int scan[kDecThreads / 32];
   KSlots slots;
   alignas(16) float dequant[kH];
@@ -96,6 +97,8 @@ __device__ __forceinline__ int pg_workers(int chunks, int ctas) {
 __device__ __forceinline__ int pg_first_chunk(int w, int chunks, int workers) {
   return static_cast<int>(static_cast<long long>(w) * chunks / workers);
 }
+// A CTA's warpgroups take consecutive ranges, as few of them as the workers need.
+__device__ __forceinline__ int pg_per_cta(int workers, int ctas) { return max(1, (workers + ctas - 1) / ctas); }
 // The warpgroup whose range holds chunk x.
 __device__ __forceinline__ int pg_worker_of(int x, int chunks, int workers) {
   return static_cast<int>(((static_cast<long long>(x) + 1) * workers - 1) / chunks);
@@ -214,10 +217,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
   const uint32_t tbase = S.tmem_base + 128u * g;            // K-hat 96 (V-hat^T in 64 of them), S 16, O 16
   const uint32_t tS = tbase + 96, tO = tbase + 112;
   const int workers = pg_workers(chunks, a.ctas);
-  const int w = g * a.ctas + cta;
+  const int per = pg_per_cta(workers, a.ctas);
+  const int w_cta = cta * per, w_end = min(w_cta + per, workers);   // this CTA's workers
+  const int w = g < per ? w_cta + g : workers;
   const int x0 = w < workers ? pg_first_chunk(w, chunks, workers) : 0;
   const int x1 = w < workers ? pg_first_chunk(w + 1, chunks, workers) : 0;
   const int b0 = x1 > x0 ? find_span(cs, a.pg.batch, x0) : 0;
+  // several workers inside one sequence leave one share, at the first one's entry
+  const bool joint = w_cta + 1 < w_end && pg_first_chunk(w_end, chunks, workers) <=
+                                              cs[find_span(cs, a.pg.batch, pg_first_chunk(w_cta, chunks, workers)) + 1];
   volatile int* abort_flag = &S.wg_abort[g];
   const size_t e0 = static_cast<size_t>(hkv) * a.entries + w;   // entry of sequence b: e0 + b
 
@@ -420,10 +428,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
         const uint8_t* kw = st + q * kbytes + lane4;
         auto put = [&](int slot, const uint32_t (&v)[4]) { tc::tmem_st<4>(tbase + lane_base + 4 * slot, v); };
         // the first columns are free already, the others held the last chunk's V-hat^T
-        k_lookup(kw, S.slots, 0, kPgVCol / 4, sm, lane4, put);
+        k_lookup(kw, S.slots, 0, kPgVCol / 4, 1, sm, lane4, put);
         if (j > 0 && !tc::mbar_wait(&S.ofull[g], (j - 1) & 1, WL)) *abort_flag = 1;
         tc::fence_after_sync();
-        k_lookup(kw, S.slots, kPgVCol / 4, kPlanSlots, sm, lane4, put);
+        k_lookup(kw, S.slots, kPgVCol / 4, kPlanSlots, 1, sm, lane4, put);
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
@@ -539,19 +547,35 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
         uint32_t o[16];
         tc::tmem_ld<16>(tO + lane_base, o);
         tc::wait_ld();
-        const size_t e = e0 + b;
-        float* po = a.part_o + e * 8 * kD + t;
-#pragma unroll
-        for (int h = 0; h < kRows; ++h)
-          if (h < a.group) po[h * kD] = (__uint_as_float(o[h]) + __uint_as_float(o[8 + h])) * (1.0f / kPgScale);
+        float l[kRows];
 #pragma unroll
         for (int h = 0; h < kRows; ++h) {
-          float l = (h & 1) ? L[h >> 1].y : L[h >> 1].x;
+          l[h] = (h & 1) ? L[h >> 1].y : L[h >> 1].x;
 #pragma unroll
-          for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-          if (lane == 0) {
-            a.part_l[(e * 4 + q) * 8 + h] = l;
-            if (q == 0) a.part_m[e * 8 + h] = seg_bad ? __int_as_float(0x7fc00000) : -((h & 1) ? nM[h >> 1].y : nM[h >> 1].x);
+          for (int k = 16; k > 0; k >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], k);
+        }
+        const float gone = __int_as_float(0x7fc00000);
+        if (joint) {
+          // the stages are free now: every copy of this warpgroup has been read
+          float* po = reinterpret_cast<float*>(my_stages) + t;
+#pragma unroll
+          for (int h = 0; h < kRows; ++h) {
+            po[h * kD] = __uint_as_float(o[h]) + __uint_as_float(o[8 + h]);
+            if (lane == 0) {
+              S.join_l[g][q][h] = l[h];
+              if (q == 0) S.join_m[g][h] = seg_bad ? gone : -((h & 1) ? nM[h >> 1].y : nM[h >> 1].x);
+            }
+          }
+        } else {
+          const size_t e = e0 + b;
+          float* po = a.part_o + e * 8 * kD + t;
+#pragma unroll
+          for (int h = 0; h < kRows; ++h) {
+            if (h < a.group) po[h * kD] = (__uint_as_float(o[h]) + __uint_as_float(o[8 + h])) * (1.0f / kPgScale);
+            if (lane == 0) {
+              a.part_l[(e * 4 + q) * 8 + h] = l[h];
+              if (q == 0) a.part_m[e * 8 + h] = seg_bad ? gone : -((h & 1) ? nM[h >> 1].y : nM[h >> 1].x);
+            }
           }
         }
       }
@@ -562,12 +586,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
     }
     if (stopped) {                                          // the segments left have no result
       if (lane == 0 && q == 0) record_status(a.status, KVQ_ERR_TIMEOUT);
-      if (q == 0 && lane < 8)
-        for (; x < x1; ++b)
-          if (cs[b + 1] > x) {
-            a.part_m[(e0 + b) * 8 + lane] = __int_as_float(0x7fc00000);
-            x = cs[b + 1];
-          }
+      if (q == 0 && lane < 8) {
+        if (joint) S.join_m[g][lane] = __int_as_float(0x7fc00000);
+        else
+          for (; x < x1; ++b)
+            if (cs[b + 1] > x) {
+              a.part_m[(e0 + b) * 8 + lane] = __int_as_float(0x7fc00000);
+              x = cs[b + 1];
+            }
+      }
     }
   }
   __syncthreads();
@@ -576,6 +603,35 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
     // (the table's copy lands before the CTA leaves, used or not)
     const bool landed = tc::mbar_wait(&S.setup, 0, WL);
     if (!landed || S.wg_abort[0] | S.wg_abort[1] | S.wg_abort[2] | S.wg_abort[3]) record_status(a.status, KVQ_ERR_TIMEOUT);
+  }
+  if (joint && !bad) {
+    // The warpgroups' shares of one sequence meet at a common maximum. A NaN maximum (a missing
+    // share) stays one.
+    const int nw = w_end - w_cta;
+    const size_t e_first = static_cast<size_t>(hkv) * a.entries + w_cta +
+                           find_span(cs, a.pg.batch, pg_first_chunk(w_cta, chunks, workers));
+    const float* share = reinterpret_cast<const float*>(sm + pg_stage_off(a.pg.batch));
+    const int pitch = NS * cbytes / 4;
+    for (int i = tid; i < a.group * kD; i += kDecThreads) {
+      const int h = i >> 7, d = i & (kD - 1);
+      float mx = -INFINITY;
+      bool missing = false;
+      for (int k = 0; k < nw; ++k) {
+        missing |= S.join_m[k][h] != S.join_m[k][h];
+        mx = fmaxf(mx, S.join_m[k][h]);
+      }
+      float os = 0.0f, ls[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < nw; ++k) {
+        // (a share of NaN logits alone has maximum -inf and a NaN sum)
+        const float wt = S.join_m[k][h] == -INFINITY ? (S.join_l[k][0][h] == 0.0f ? 0.0f : S.join_l[k][0][h]) : fast_exp2(S.join_m[k][h] - mx);
+        os += wt * share[k * pitch + h * kD + d];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) ls[r] += wt * S.join_l[k][r][h];
+      }
+      a.part_o[(e_first * 8 + h) * kD + d] = os * (1.0f / kPgScale);
+      if (d < 4) a.part_l[(e_first * 4 + d) * 8 + h] = d == 0 ? ls[0] : d == 1 ? ls[1] : d == 2 ? ls[2] : ls[3];
+      if (d == 0) a.part_m[e_first * 8 + h] = missing ? __int_as_float(0x7fc00000) : mx;
+    }
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -589,7 +645,7 @@ struct MergeArgs {
   void* out;
   int out_dtype, n_q_heads, n_kv_heads, group, batch;
   const int2* plan;
-  int entries;
+  int entries, ctas;
   const float *own_m, *own_l, *own_o;      // as PagedAttn's part_*
   int prefix_len, pre_groups, pre_splits;
   const float *pre_m, *pre_l, *pre_o;      // [CTA][kPreRows], ..., CTA = (split * groups + group) * heads + head
@@ -597,25 +653,40 @@ struct MergeArgs {
 
 constexpr int kPreRows = 128;              // query rows of a CTA on the prefix
 
-constexpr int kMergeWarps = 16;
+constexpr int kMergeWarps = 16;            // at most
 
 // One CTA joins the shares of one (sequence, query head): the prefix's splits, then the
-// sequence's own. Warp w folds shares w, w + 16, .. with its own running maximum (lane = 4 dims,
+// sequence's own. Warp w of n folds shares w, w + n, .. with its own running maximum (lane = 4 dims,
 // the loads of eight shares in flight), then the warps meet in shared memory. The order of the
 // sums is fixed. A NaN maximum marks a missing share: the row is left as it is.
+// The host gives few rows 16 warps each and many rows 4.
 __global__ void __launch_bounds__(kMergeWarps * 32) kvq_paged_merge(const MergeArgs a) {
   __shared__ float sm_m[kMergeWarps], sm_l[kMergeWarps];
   __shared__ float4 sm_o[kMergeWarps][32];
   const int hq = blockIdx.x % a.n_q_heads, b = blockIdx.x / a.n_q_heads;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_warps = blockDim.x >> 5;
   const int hkv = hq / a.group, h = hq - hkv * a.group;
   grid_dependency_wait();
   const int2 plan = __ldcg(a.plan + b), all = __ldcg(a.plan + a.batch);
   if (plan.y < 0) return;                                    // refused
-  int w0 = 0, n_own = 0;
+  // own shares: workers w0 .. of the first CTAs one by one, CTAs c_lo .. c_hi - 1 whose workers all
+  // lie in the sequence by their first, the rest one by one
+  int w0 = 0, n_own = 0, n_lo = 0, n_mid = 0, per = 1, w_mid = 0;
   if (plan.y > 0) {
     w0 = pg_worker_of(plan.x, all.x, all.y);
-    n_own = pg_worker_of(plan.x + plan.y - 1, all.x, all.y) - w0 + 1;
+    const int w_end = pg_worker_of(plan.x + plan.y - 1, all.x, all.y) + 1;
+    per = pg_per_cta(all.y, a.ctas);
+    int c_lo = w0 / per, c_hi = (w_end + per - 1) / per;
+    if (pg_first_chunk(c_lo * per, all.x, all.y) < plan.x) ++c_lo;
+    if (pg_first_chunk(min(c_hi * per, all.y), all.x, all.y) > plan.x + plan.y) --c_hi;
+    n_mid = max(0, c_hi - c_lo);
+    if (n_mid > 0) {
+      w_mid = c_lo * per;
+      n_lo = w_mid - w0;
+      n_own = n_lo + n_mid + max(0, w_end - c_hi * per);
+    } else {
+      n_lo = n_own = w_end - w0;
+    }
   }
   const int n_pre = a.prefix_len > 0 ? a.pre_splits : 0;
   const int n = n_pre + n_own;
@@ -624,12 +695,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kvq_paged_merge(const MergeA
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   bool missing = false;
   constexpr int kBatch = 8;
-  for (int i0 = warp; i0 < n; i0 += kMergeWarps * kBatch) {
+  for (int i0 = warp; i0 < n; i0 += n_warps * kBatch) {
     float mv[kBatch], lv[kBatch];
     float4 ov[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int i = i0 + kMergeWarps * u;
+      const int i = i0 + n_warps * u;
       mv[u] = -INFINITY;
       lv[u] = 0.0f;
       ov[u] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -639,7 +710,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kvq_paged_merge(const MergeA
         lv[u] = __ldcg(a.pre_l + e);
         ov[u] = __ldcg(reinterpret_cast<const float4*>(a.pre_o + e * kD) + lane);
       } else if (i < n) {
-        const size_t e = static_cast<size_t>(hkv) * a.entries + w0 + (i - n_pre) + b;
+        const int k = i - n_pre;
+        const int w = k < n_lo ? w0 + k : k < n_lo + n_mid ? w_mid + (k - n_lo) * per : w_mid + n_mid * per + (k - n_lo - n_mid);
+        const size_t e = static_cast<size_t>(hkv) * a.entries + w + b;
         mv[u] = __ldcg(a.own_m + e * 8 + h);
         const float* l = a.own_l + e * 32 + h;
         lv[u] = (__ldcg(l) + __ldcg(l + 8)) + (__ldcg(l + 16) + __ldcg(l + 24));
@@ -676,10 +749,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kvq_paged_merge(const MergeA
   if (threadIdx.x >= kD) return;
   const int d = threadIdx.x;
   float mx = -INFINITY, Ls = 0.0f, Os = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) mx = fmaxf(mx, sm_m[w]);
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
+  for (int w = 0; w < n_warps; ++w) mx = fmaxf(mx, sm_m[w]);
+  for (int w = 0; w < n_warps; ++w) {
     if (sm_m[w] == -INFINITY) {
       if (sm_l[w] != sm_l[w]) Ls = sm_l[w];
       continue;

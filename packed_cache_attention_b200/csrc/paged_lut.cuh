@@ -117,18 +117,18 @@ __device__ __forceinline__ void k_wide_vals(uint32_t r0, uint32_t r1, const uint
   }
 }
 
-// K-hat columns of slots first .. end - 1 (at most S.n) of the lane's token; kw: its word 0 (word i at
-// byte 128 i). put(slot, v) takes a slot's 4 columns. Narrow slots of every width go through one
+// K-hat columns of slots first, first + step, .. below end (at most S.n) of the lane's token; kw: its
+// word 0 (word i at byte 128 i). put(slot, v) takes a slot's 4 columns. Narrow slots of every width go through one
 // sequence of instructions, two at a time. Words past the stream are read inside the stage and not
 // used.
 template <typename Put>
-__device__ __forceinline__ void k_lookup(const uint8_t* kw, const KSlots& S, int first, int end, const uint8_t* lut,
-                                         uint32_t lane4, Put put) {
+__device__ __forceinline__ void k_lookup(const uint8_t* kw, const KSlots& S, int first, int end, int step,
+                                         const uint8_t* lut, uint32_t lane4, Put put) {
   end = min(end, S.n);
   const int wide_end = min(end, S.n_wide);
   int s = first;
 #pragma unroll 1
-  for (; s < wide_end; ++s) {
+  for (; s < wide_end; s += step) {
     const uint4 d = S.a[s];
     const uint32_t* p = reinterpret_cast<const uint32_t*>(kw + static_cast<int>(d.x));
     const uint32_t x0 = p[0], x1 = p[32], x2 = p[64];
@@ -140,9 +140,8 @@ __device__ __forceinline__ void k_lookup(const uint8_t* kw, const KSlots& S, int
     put(s, v);
   }
 #pragma unroll 1
-  for (; s < end; s += 2) {
-    // (an odd number of slots: the last is looked up twice)
-    const int k1 = min(s + 1, end - 1);
+  for (; s < end; s += 2 * step) {
+    const int k1 = s + step < end ? s + step : s;      // (an odd number of slots: the last is looked up twice)
     const uint4 d[2] = {S.a[s], S.a[k1]};
     const uint2 b[2] = {S.b[s], S.b[k1]};
     uint32_t v[2][4];

@@ -8,7 +8,8 @@
 //
 // Precision: Q' and P' are fp16 high + low parts (Khat and Vhat are fp16 centroids, exact), so every
 // product runs twice; the norms of keys and values multiply the fp32 logits and shares. A
-// single fp16 Q' would move a logit of 100 by 2^-5.
+// single fp16 Q' would move a logit of 100 by 2^-5. For bf16 outputs P' has its high part alone: a
+// share is then off by at most 2^-11 of itself, a quarter of the output's own rounding (2^-9).
 //
 // Layout. Tensor memory: Q' high (A operand, 96 columns), two buffers of 128 columns for S, O. A
 // warpgroup writes its P' over the S columns that it has read (16 columns high parts, 16 low).
@@ -40,6 +41,7 @@ struct PrefixArgs {
   PagedArgs pg;
   const int32_t* pages;                   // the prefix's pages
   int len, splits, row_groups, n_stages;
+  int low_p;                              // P' has low parts
   float* part_m;                          // [CTA][kPreRows]
   float* part_l;
   float* part_o;                          // [CTA][kPreRows][128]
@@ -231,6 +233,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
         const uint32_t p = tb + kPreS + 128u * (j & 1);
 #pragma unroll
         for (int ks = 0; ks < 2 * (kChunkTokens / 16); ++ks) {
+          if (ks >= kChunkTokens / 16 && !a.low_p) break;
           const int kk = ks % (kChunkTokens / 16);          // high parts, then low parts
           tc::mma_ts(tb + kPreO, p + 32 * (kk >> 1) + 8 * (kk & 1) + (ks >= kChunkTokens / 16 ? 16 : 0),
                      tc::sdesc(bv + 4096 * kk, 2048, 128), id, (j > 0 || ks > 0) ? 1u : 0u);
@@ -306,7 +309,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
     named_sync(1, 512);                                     // the staged rows are read
     if (!tc::mbar_wait(&S.setup, 0, WL)) *abort_flag = 1;
 
-    // Khat(j) and the norms of its tokens (lane = token; a warpgroup takes a quarter of the slots)
+    // Khat(j) and the norms of its tokens (lane = token; a warpgroup takes every fourth slot)
     Ring rk, rv;
     auto keys = [&](int j) {
       const int s = rk.s;
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
       rk.next(NS);
       const uint8_t* rec = stages + static_cast<size_t>(s) * cbytes + q * kbytes;
       const uint8_t* kw = rec + lane4;
-      k_lookup(kw, S.slots, S.slots.n * wg / 4, S.slots.n * (wg + 1) / 4, sm, lane4, [&](int slot, const uint32_t (&v)[4]) {
+      k_lookup(kw, S.slots, wg, kPlanSlots, 4, sm, lane4, [&](int slot, const uint32_t (&v)[4]) {
         *reinterpret_cast<uint4*>(sm + kPreKOff + slot * 2048 + t * 16) = make_uint4(v[0], v[1], v[2], v[3]);
       });
       if (wg == (j & 3)) {
@@ -398,30 +401,37 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
           }
         }
         // ---------------------------------------------------------- P', over the S columns just read
-        const float2 qs2 = make_float2(qs, qs), nM = make_float2(-M, -M), minus1 = make_float2(-1.0f, -1.0f);
+        const float2 qs2 = make_float2(qs, qs), nM = make_float2(-M, -M);
         const float4* vn = reinterpret_cast<const float4*>(S.norm[j & 1][1] + 32 * wg);
-        uint32_t hi[16], lo[16];
         float2 sum = make_float2(0.0f, 0.0f);
+        uint32_t hi[16];
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
           const float4 f = vn[i >> 2];
-          const float2 fv[2] = {make_float2(f.x, f.y), make_float2(f.z, f.w)};
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float2 z = fma2(make_float2(x[i + 2 * k], x[i + 2 * k + 1]), qs2, nM);
+          for (int k = i; k < i + 4; k += 2) {
+            const float2 z = fma2(make_float2(x[k], x[k + 1]), qs2, nM);
             const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
             sum = add2(sum, p);
-            const float2 y = mul2(p, fv[k]);
+            const float2 y = mul2(p, k == i ? make_float2(f.x, f.y) : make_float2(f.z, f.w));
             const __half2 yh = __floats2half2_rn(y.x, y.y);
-            const float2 r = fma2(__half22float2(yh), minus1, y);
-            const __half2 yl = __floats2half2_rn(r.x, r.y);
-            hi[(i >> 1) + k] = *reinterpret_cast<const uint32_t*>(&yh);
-            lo[(i >> 1) + k] = *reinterpret_cast<const uint32_t*>(&yl);
+            hi[k >> 1] = *reinterpret_cast<const uint32_t*>(&yh);
+            x[k] = y.x;
+            x[k + 1] = y.y;
           }
         }
-        L += sum.x + sum.y;
         tc::tmem_st<16>(tS, hi);
-        tc::tmem_st<16>(tS + 16, lo);
+        if (a.low_p) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const float2 r = fma2(__half22float2(*reinterpret_cast<const __half2*>(&hi[k >> 1])), make_float2(-1.0f, -1.0f),
+                                  make_float2(x[k], x[k + 1]));
+            const __half2 yl = __floats2half2_rn(r.x, r.y);
+            hi[k >> 1] = *reinterpret_cast<const uint32_t*>(&yl);
+          }
+          tc::tmem_st<16>(tS + 16, hi);
+        }
+        L += sum.x + sum.y;
       }
       // ------------------------------------------------------------ values (lane = dim, one tile a warpgroup)
       const int s = rv.s;
