@@ -1028,6 +1028,18 @@ kvq_status launch_append_bv(const PagedArgs& a, const PagedQuant& p, const RopeA
   }
 }
 
+// True if dynamic shared memory begins where the paged attention kernels' lookup tables need it.
+bool smem_base_ok() {
+  static std::atomic<int> cached[kMaxDevices];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  if ((n = cached[dev].load(std::memory_order_relaxed)) == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrReservedSharedMemoryPerBlock, dev) != cudaSuccess) return false;
+    cached[dev].store(n, std::memory_order_relaxed);
+  }
+  return n == static_cast<int>(kSmemBase);
+}
+
 // CTAs per KV head of a paged decode: one per SM in all (a head has one at least).
 int paged_ctas(int n_kv_heads) { return std::max(1, sm_count() / n_kv_heads); }
 
@@ -1226,10 +1238,10 @@ kvq_status kvq_paged_decode_attn(const void* q, const kvq_tensor4* qd, const voi
   const int group = qd->n_heads / d->n_kv_heads;
   const PagedWs w = paged_ws(seqs->batch, d->n_kv_heads, group, plen > 0);
   if (!ws || ws_bytes < w.total || !aligned16(ws)) return KVQ_ERR_WORKSPACE;
-  const size_t cb = 4ull * chunk_bytes(pg.rec_bytes), room = max_smem() - pg_stage_off(seqs->batch);
+  const size_t cb = 4ull * chunk_bytes(pg.rec_bytes), room = max_smem() - kPgStageOff;
   const int n_stages = static_cast<int>(std::min<size_t>(kPgStagesMax, room / cb));
-  if (n_stages < 1) return KVQ_ERR_UNSUPPORTED;
-  const size_t smem = pg_stage_off(seqs->batch) + n_stages * cb;
+  if (n_stages < 1 || !smem_base_ok()) return KVQ_ERR_UNSUPPORTED;
+  const size_t smem = kPgStageOff + n_stages * cb;
   if ((st = ensure_tables()) != KVQ_OK) return st;
   uint8_t* w8 = static_cast<uint8_t*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -68,14 +68,16 @@ struct PgHeader {
   alignas(4) int8_t col_of[kH];            // column of a block (-1: width 0)
 };
 
-// Shared memory: lookup tables, Q' and P' of each warpgroup, header, chunk offsets, stages.
+// Shared memory: Q' of each warpgroup, header, chunk offsets; lookup tables (at their address);
+// P', stages.
 constexpr int kPgQBytes = 6144;            // 192 K elements x 16 rows
 constexpr int kPgPBytes = 4096;            // 128 tokens x 16 rows
-constexpr int kPgQOff = kPlutBytes;
-constexpr int kPgPOff = kPgQOff + 4 * kPgQBytes;
-constexpr int kPgHdrOff = kPgPOff + 4 * kPgPBytes;
+constexpr int kPgQOff = 0;
+constexpr int kPgHdrOff = kPgQOff + 4 * kPgQBytes;
 constexpr int kPgScanOff = kPgHdrOff + (static_cast<int>(sizeof(PgHeader)) + 15) / 16 * 16;
-__host__ __device__ constexpr int pg_stage_off(int batch) { return (kPgScanOff + 4 * (batch + 1) + 127) / 128 * 128; }
+static_assert(kPgScanOff + 4 * (kPagedMaxBatch + 1) <= kPlutAt, "before the lookup tables");
+constexpr int kPgPOff = kPlutEnd;
+constexpr int kPgStageOff = kPgPOff + 4 * kPgPBytes;
 
 // Place in a ring of stages and the parity of its phase.
 struct Ring {
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
   const bool is_issuer = warp >= kDecIssuerWarp0;
   const int g = is_issuer ? warp - kDecIssuerWarp0 : warp >> 2;
   const int q = warp & 3;
-  uint8_t* my_stages = sm + pg_stage_off(a.pg.batch) + static_cast<size_t>(g) * NS * cbytes;   // K of a chunk, then V
+  uint8_t* my_stages = sm + kPgStageOff + static_cast<size_t>(g) * NS * cbytes;   // K of a chunk, then V
 
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
@@ -169,10 +171,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
       S.wg_stop[i] = 0;
     }
     tc::mbar_init(&S.setup, 1);
-    S.bad = 0;
+    S.bad = tc::smem_u32(sm) != kSmemBase;                  // the tables would not be at their address
+    if (S.bad) record_status(a.status, KVQ_ERR_UNSUPPORTED);
     tc::mbar_fence_init();
     tc::mbar_arrive_expect_tx(&S.setup, kPlutBytes);
-    tc::bulk_g2s(sm, g_paged_lut, kPlutBytes, &S.setup);
+    tc::bulk_g2s(sm + kPlutAt, g_paged_lut, kPlutBytes, &S.setup);
   }
   if (warp == kDecIssuerWarp0) tc::tmem_alloc(&S.tmem_base, kTmemCols);
   for (int i = tid; i < 4 * kPgQBytes / 16; i += kDecThreads)
@@ -354,7 +357,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
   } else {
     // ------------------------------------------------------------------ compute warps
     const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
-    const uint32_t lane4 = static_cast<uint32_t>(lane) << 2;
+    const uint32_t lane4 = static_cast<uint32_t>(lane) << 2, tab = plut_lane(VM, lane);
     const int t = 32 * q + lane;                            // token of a chunk, dim of a value, thread of the warpgroup
     uint8_t* pb = sm + kPgPOff + g * kPgPBytes + (t >> 3) * 256 + (t & 7) * 16;
     uint8_t* qb = sm + kPgQOff + g * kPgQBytes;
@@ -428,10 +431,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
         const uint8_t* kw = st + q * kbytes + lane4;
         auto put = [&](int slot, const uint32_t (&v)[4]) { tc::tmem_st<4>(tbase + lane_base + 4 * slot, v); };
         // the first columns are free already, the others held the last chunk's V-hat^T
-        k_lookup(kw, S.slots, 0, kPgVCol / 4, 1, sm, lane4, put);
+        k_lookup(kw, S.slots, 0, kPgVCol / 4, 1, lane4, put);
         if (j > 0 && !tc::mbar_wait(&S.ofull[g], (j - 1) & 1, WL)) *abort_flag = 1;
         tc::fence_after_sync();
-        k_lookup(kw, S.slots, kPgVCol / 4, kPlanSlots, 1, sm, lane4, put);
+        k_lookup(kw, S.slots, kPgVCol / 4, kPlanSlots, 1, lane4, put);
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
@@ -447,14 +450,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
         {
           uint32_t v16[16];
           const uint32_t* vw = reinterpret_cast<const uint32_t*>(sv + 4 * kTile) + t;
-          v_vals<VM>(vw, sm, lane4, v16);
+          v_vals<VM>(vw, tab, v16);
           if (!tc::mbar_wait(&S.sfull[g], j & 1, WL)) *abort_flag = 1;   // K-hat is read
           tc::fence_after_sync();
           tc::tmem_st<16>(tbase + kPgVCol + lane_base, v16);
 #pragma unroll
           for (int u = 1; u < kChunkTiles; ++u) {
             vw = reinterpret_cast<const uint32_t*>(sv + u * vbytes + 4 * kTile) + t;
-            v_vals<VM>(vw, sm, lane4, v16);
+            v_vals<VM>(vw, tab, v16);
             tc::tmem_st<16>(tbase + kPgVCol + lane_base + 16 * u, v16);
           }
         }
@@ -610,7 +613,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
     const int nw = w_end - w_cta;
     const size_t e_first = static_cast<size_t>(hkv) * a.entries + w_cta +
                            find_span(cs, a.pg.batch, pg_first_chunk(w_cta, chunks, workers));
-    const float* share = reinterpret_cast<const float*>(sm + pg_stage_off(a.pg.batch));
+    const float* share = reinterpret_cast<const float*>(sm + kPgStageOff);
     const int pitch = NS * cbytes / 4;
     for (int i = tid; i < a.group * kD; i += kDecThreads) {
       const int h = i >> 7, d = i & (kD - 1);

@@ -15,9 +15,11 @@
 
 namespace kvq {
 
-// Byte offsets of the tables.
+// Byte offsets of the tables, each a multiple of its size. The image sits at a shared-memory
+// address that is a multiple of 32 KB (plut_place), so that a field, the lane and a table's
+// address have no bits in common.
 __host__ __device__ constexpr int plut_off(int w) {
-  return w == 4 ? 0 : w == 3 ? 32768 : w == 2 ? 40960 : w == 1 ? 43008 : w == 6 ? 43520 : w == 7 ? 43648 : w == 8 ? 44032 : 45056;
+  return w == 4 ? 0 : w == 3 ? 32768 : w == 2 ? 40960 : w == 1 ? 43008 : w == 8 ? 43520 : w == 7 ? 44032 : w == 6 ? 44288 : 45056;
 }
 constexpr int kPlutBytes = 49152;
 
@@ -39,6 +41,26 @@ inline void paged_lut_image(const uint16_t* c16, uint8_t* img) {
 }
 
 __device__ __align__(16) uint8_t g_paged_lut[kPlutBytes];
+
+// Dynamic shared memory of a kernel without static variables begins behind the 1 KB that the system
+// keeps (the host checks that, the kernels too); the image begins 32 KB into the window.
+constexpr uint32_t kSmemBase = 1024, kPlutAddr = 32768;
+constexpr int kPlutAt = kPlutAddr - kSmemBase, kPlutEnd = kPlutAt + kPlutBytes;   // from the start of dynamic shared memory
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+// Address of width w's table as this lane uses it.
+__device__ __forceinline__ uint32_t plut_lane(int w, uint32_t lane) {
+  return kPlutAddr + static_cast<uint32_t>(plut_off(w)) + (w <= 4 ? 4u * lane : 0u);
+}
 
 // ---------------------------------------------------------------- keys
 
@@ -69,7 +91,7 @@ __device__ __forceinline__ bool k_slots(const uint32_t* slots, int n_cols, int s
   if (s < n) {
     S.a[s] = make_uint4(static_cast<uint32_t>((at >> 5) * 128), static_cast<uint32_t>(at) & 31u, w <= 5 ? 2 * w : w,
                         w <= 5 ? ((1u << (2 * w)) - 1u) << (w <= 4 ? 7 : 2) : 0u);
-    S.b[s] = make_uint2(static_cast<uint32_t>(plut_off(static_cast<int>(w))), w <= 4 ? 0x7cu : 0u);
+    S.b[s] = make_uint2(kPlutAddr + static_cast<uint32_t>(plut_off(static_cast<int>(w))), w <= 4 ? 0x7cu : 0u);
   }
   if (s == 0) {
     S.n_wide = n_wide;
@@ -80,22 +102,18 @@ __device__ __forceinline__ bool k_slots(const uint32_t* slots, int n_cols, int s
 
 // ---------------------------------------------------------------- values
 
+// Two consecutive codes of width W at bit p of hi:lo; `tab` = plut_lane(W, lane).
 template <int W>
-__device__ __forceinline__ uint32_t pair_of(uint32_t lo, uint32_t hi, int p, const uint8_t* lut, uint32_t lane4) {
-  if constexpr (W <= 4) {
-    return *reinterpret_cast<const uint32_t*>(lut + plut_off(W) + (field_at(lo, hi, p, 2 * W, 7) | lane4));
-  } else if constexpr (W == 5) {
-    return *reinterpret_cast<const uint32_t*>(lut + plut_off(W) + field_at(lo, hi, p, 2 * W, 2));
-  } else {
-    const uint8_t* t = lut + plut_off(W);
-    return static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(t + field_at(lo, hi, p, W, 1))) |
-           (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(t + field_at(lo, hi, p + W, W, 1))) << 16);
-  }
+__device__ __forceinline__ uint32_t pair_of(uint32_t lo, uint32_t hi, int p, uint32_t tab) {
+  if constexpr (W <= 4) return lds32(field_at(lo, hi, p, 2 * W, 7) | tab);
+  else if constexpr (W == 5) return lds32(field_at(lo, hi, p, 2 * W, 2) | tab);
+  else return lds16(field_at(lo, hi, p, W, 1) | tab) | lds16(field_at(lo, hi, p + W, W, 1) | tab) << 16;
 }
 
-// V-hat of one dim for the 32 tokens of a tile: 16 token pairs (2u, 2u + 1). vw: word 0 of the dim.
+// V-hat of one dim for the 32 tokens of a tile: 16 token pairs (2u, 2u + 1). vw: word 0 of the
+// dim, tab: plut_lane(BV, lane).
 template <int BV>
-__device__ __forceinline__ void v_vals(const uint32_t* vw, const uint8_t* lut, uint32_t lane4, uint32_t (&v)[16]) {
+__device__ __forceinline__ void v_vals(const uint32_t* vw, uint32_t tab, uint32_t (&v)[16]) {
   uint32_t x[BV + 1];
 #pragma unroll
   for (int i = 0; i < BV; ++i) x[i] = vw[i * kD];
@@ -103,17 +121,17 @@ __device__ __forceinline__ void v_vals(const uint32_t* vw, const uint8_t* lut, u
 #pragma unroll
   for (int u = 0; u < 16; ++u) {
     const int p = 2 * BV * u;
-    v[u] = pair_of<BV>(x[p >> 5], x[(p >> 5) + 1], p & 31, lut, lane4);
+    v[u] = pair_of<BV>(x[p >> 5], x[(p >> 5) + 1], p & 31, tab);
   }
 }
 
 // The 4 words of one wide slot from its two aligned stream words.
 template <int W>
-__device__ __forceinline__ void k_wide_vals(uint32_t r0, uint32_t r1, const uint8_t* lut, uint32_t (&v)[4]) {
+__device__ __forceinline__ void k_wide_vals(uint32_t r0, uint32_t r1, uint32_t (&v)[4]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int p = 2 * W * k;
-    v[k] = p < 32 ? pair_of<W>(r0, r1, p, lut, 0u) : pair_of<W>(r1, 0u, p - 32, lut, 0u);
+    v[k] = p < 32 ? pair_of<W>(r0, r1, p, kPlutAddr + plut_off(W)) : pair_of<W>(r1, 0u, p - 32, kPlutAddr + plut_off(W));
   }
 }
 
@@ -123,7 +141,7 @@ __device__ __forceinline__ void k_wide_vals(uint32_t r0, uint32_t r1, const uint
 // used.
 template <typename Put>
 __device__ __forceinline__ void k_lookup(const uint8_t* kw, const KSlots& S, int first, int end, int step,
-                                         const uint8_t* lut, uint32_t lane4, Put put) {
+                                         uint32_t lane4, Put put) {
   end = min(end, S.n);
   const int wide_end = min(end, S.n_wide);
   int s = first;
@@ -134,9 +152,9 @@ __device__ __forceinline__ void k_lookup(const uint8_t* kw, const KSlots& S, int
     const uint32_t x0 = p[0], x1 = p[32], x2 = p[64];
     const uint32_t r0 = __funnelshift_r(x0, x1, d.y), r1 = __funnelshift_r(x1, x2, d.y);
     uint32_t v[4];
-    if (d.z == 6) k_wide_vals<6>(r0, r1, lut, v);
-    else if (d.z == 7) k_wide_vals<7>(r0, r1, lut, v);
-    else k_wide_vals<8>(r0, r1, lut, v);
+    if (d.z == 6) k_wide_vals<6>(r0, r1, v);
+    else if (d.z == 7) k_wide_vals<7>(r0, r1, v);
+    else k_wide_vals<8>(r0, r1, v);
     put(s, v);
   }
 #pragma unroll 1
@@ -154,7 +172,7 @@ __device__ __forceinline__ void k_lookup(const uint8_t* kw, const KSlots& S, int
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t f = (k == 0) ? r0 : __funnelshift_r(r0, r1, d[u].z * k);
-        v[u][k] = *reinterpret_cast<const uint32_t*>(lut + ((f & d[u].w) | lb));
+        v[u][k] = lds32((f & d[u].w) | lb);
       }
     }
     put(s, v[0]);

@@ -63,26 +63,31 @@ struct PreHeader {
   float xch[2][4][kPreRows];                    // [chunk parity][warpgroup][row]: maximum; sums at the end
 };
 
-constexpr int kPreQOff = kPlutBytes;                 // Q' low
-constexpr int kPreKOff = kPreQOff + 192 * kPreRows * 2;
+// Shared memory: header, Q' low of the first kPreQCut K steps; lookup tables (at their address); Q'
+// low of the other steps, Khat, Vhat, stages.
+constexpr int kPreHdrOff = 0, kPreQCut = 5;
+constexpr int kPreQ0 = kPreHdrOff + (static_cast<int>(sizeof(PreHeader)) + 127) / 128 * 128;
+static_assert(kPreQ0 + kPreQCut * 4096 <= kPlutAt, "before the lookup tables");
+constexpr int kPreQ1 = kPlutEnd;
+constexpr int kPreKOff = kPreQ1 + (12 - kPreQCut) * 4096;
 constexpr int kPreVOff = kPreKOff + 192 * kChunkTokens * 2;
-constexpr int kPreHdrOff = kPreVOff + kD * kChunkTokens * 2;
-constexpr int kPreStageOff = kPreHdrOff + (static_cast<int>(sizeof(PreHeader)) + 127) / 128 * 128;
+constexpr int kPreStageOff = kPreVOff + kD * kChunkTokens * 2;
+__device__ __forceinline__ int pre_q_step(int ks) { return ks < kPreQCut ? kPreQ0 + 4096 * ks : kPreQ1 + 4096 * (ks - kPreQCut); }
 constexpr int kPreQPitch = kD + 1;                   // staged fp32 queries, over Khat and Vhat before the first chunk
-static_assert(kPreRows * kPreQPitch * 4 <= kPreHdrOff - kPreKOff, "staged queries");
+static_assert(kPreRows * kPreQPitch * 4 <= kPreStageOff - kPreKOff, "staged queries");
 constexpr uint32_t kPreS = 96, kPreO = 352;          // tensor-memory columns (Q' high at 0)
 
 // V-hat values of one tile for a run-time width.
-__device__ __forceinline__ void v_vals_any(int bv, const uint32_t* vw, const uint8_t* lut, uint32_t lane4, uint32_t (&v)[16]) {
+__device__ __forceinline__ void v_vals_any(int bv, const uint32_t* vw, uint32_t tab, uint32_t (&v)[16]) {
   switch (bv) {
-    case 1: v_vals<1>(vw, lut, lane4, v); break;
-    case 2: v_vals<2>(vw, lut, lane4, v); break;
-    case 3: v_vals<3>(vw, lut, lane4, v); break;
-    case 4: v_vals<4>(vw, lut, lane4, v); break;
-    case 5: v_vals<5>(vw, lut, lane4, v); break;
-    case 6: v_vals<6>(vw, lut, lane4, v); break;
-    case 7: v_vals<7>(vw, lut, lane4, v); break;
-    default: v_vals<8>(vw, lut, lane4, v); break;
+    case 1: v_vals<1>(vw, tab, v); break;
+    case 2: v_vals<2>(vw, tab, v); break;
+    case 3: v_vals<3>(vw, tab, v); break;
+    case 4: v_vals<4>(vw, tab, v); break;
+    case 5: v_vals<5>(vw, tab, v); break;
+    case 6: v_vals<6>(vw, tab, v); break;
+    case 7: v_vals<7>(vw, tab, v); break;
+    default: v_vals<8>(vw, tab, v); break;
   }
 }
 
@@ -115,12 +120,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
     tc::mbar_init(&S.ofull, 1);
     tc::mbar_init(&S.drain, 1);
     tc::mbar_init(&S.setup, 1);
-    S.bad = 0;
+    S.bad = tc::smem_u32(sm) != kSmemBase;                  // the tables would not be at their address
+    if (S.bad) record_status(a.status, KVQ_ERR_UNSUPPORTED);
     S.bad_page = 0;
     S.abort = 0;
     tc::mbar_fence_init();
     tc::mbar_arrive_expect_tx(&S.setup, kPlutBytes);
-    tc::bulk_g2s(sm, g_paged_lut, kPlutBytes, &S.setup);
+    tc::bulk_g2s(sm + kPlutAt, g_paged_lut, kPlutBytes, &S.setup);
   }
   if (is_issuer) tc::tmem_alloc(&S.tmem_base, kTmemCols);
   __syncthreads();
@@ -207,7 +213,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
       return r != 0;
     };
     const uint32_t id = tc::idesc_f16(128, 128, false);
-    const uint32_t aq = tc::smem_u32(sm + kPreQOff), bk = tc::smem_u32(sm + kPreKOff), bv = tc::smem_u32(sm + kPreVOff);
+    const uint32_t smb = tc::smem_u32(sm), bk = tc::smem_u32(sm + kPreKOff), bv = tc::smem_u32(sm + kPreVOff);
     auto logits = [&](int j) {                              // S(j), once Khat(j) is there
       if (!wait_warp(&S.kready, j & 1)) return false;
       if (j >= 2 && !wait_warp(&S.ofull, j & 1)) return false;        // P'(j - 2) in its buffer is read
@@ -217,7 +223,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
         for (int ks = 0; ks < k_steps; ++ks)
           tc::mma_ts(d, tb + 8 * ks, tc::sdesc(bk + 4096 * ks, 2048, 128), id, ks > 0 ? 1u : 0u);
         for (int ks = 0; ks < k_steps; ++ks)
-          tc::mma_ss(d, tc::sdesc(aq + 4096 * ks, 2048, 128), tc::sdesc(bk + 4096 * ks, 2048, 128), id, 1u);
+          tc::mma_ss(d, tc::sdesc(smb + pre_q_step(ks), 2048, 128), tc::sdesc(bk + 4096 * ks, 2048, 128), id, 1u);
         tc::mma_commit(&S.sfull);
       }
       __syncwarp();
@@ -257,7 +263,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
   } else {
     // ------------------------------------------------------------------ compute warps
     const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
-    const uint32_t lane4 = static_cast<uint32_t>(lane) << 2;
+    const uint32_t lane4 = static_cast<uint32_t>(lane) << 2, tab = plut_lane(a.pg.bits_v, lane);
     const int t = 32 * q + lane;                            // row of S and O, token of Khat, dim of Vhat
     const bool live = 32 * q < rows;                        // some row of the warp is a query
     // -------------------------------------------------------------- Q'
@@ -301,7 +307,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
         lo[c] = l0 | (l1 << 16);
       }
       tc::tmem_st<8>(tb + lane_base + 24 * wg + c8, hi);
-      uint8_t* p = sm + kPreQOff + (24 * wg + c8) / 4 * 2048 + t * 16;
+      uint8_t* p = sm + pre_q_step((24 * wg + c8) / 8) + t * 16;
       *reinterpret_cast<uint4*>(p) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       *reinterpret_cast<uint4*>(p + 2048) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
     }
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
       rk.next(NS);
       const uint8_t* rec = stages + static_cast<size_t>(s) * cbytes + q * kbytes;
       const uint8_t* kw = rec + lane4;
-      k_lookup(kw, S.slots, wg, kPlanSlots, 4, sm, lane4, [&](int slot, const uint32_t (&v)[4]) {
+      k_lookup(kw, S.slots, wg, kPlanSlots, 4, lane4, [&](int slot, const uint32_t (&v)[4]) {
         *reinterpret_cast<uint4*>(sm + kPreKOff + slot * 2048 + t * 16) = make_uint4(v[0], v[1], v[2], v[3]);
       });
       if (wg == (j & 3)) {
@@ -440,7 +446,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
       uint32_t v16[16];
       v_vals_any(a.pg.bits_v,
                  reinterpret_cast<const uint32_t*>(stages + static_cast<size_t>(s) * cbytes + kChunkTiles * kbytes + wg * vbytes) + t,
-                 sm, lane4, v16);
+                 tab, v16);
       if (j > 0 && !tc::mbar_wait(&S.ofull, (j - 1) & 1, WL)) *abort_flag = 1;   // Vhat of the last chunk is read
 #pragma unroll
       for (int i = 0; i < 4; ++i)
