@@ -1010,7 +1010,7 @@ kvq_status launch_append(const PagedArgs& a, const PagedQuant& p, const RopeArgs
   const kvq_status st = opt.raise(kvq_paged_quant<DT, BV>, smem);
   if (st != KVQ_OK) return st;
   constexpr int qw = QTile<DT>::kWarps;
-  const unsigned grid = static_cast<unsigned>(std::min<long long>(sm_count(), (max_tasks + qw - 1) / qw));
+  const unsigned grid = static_cast<unsigned>(std::min<long long>(sm_count(), max_tasks));
   const cudaError_t e = launch_pdl(kvq_paged_quant<DT, BV>, dim3(grid), dim3(qw * 32), smem, s, a, p, r);
   return e == cudaSuccess ? launch_status() : cuda_fail(e);
 }
