@@ -97,22 +97,42 @@ __device__ __forceinline__ bool outside(const RopeArgs& r, int2 p) {
          (static_cast<unsigned>(p.y) >= static_cast<unsigned>(r.n_positions));
 }
 
-// Rotates rows r_lo .. r_hi - 1 of a staged K tile in place; row r_lo is token tok0 of the call. The
-// angles of 16 rows are in flight at a time (of 4: 40 us more on 131072 tokens x 2 heads, nearly all
-// of it latency). True if a position was outside the table.
+// Rotates rows r_lo .. r_hi - 1 of a staged K tile in place; row r_lo is token tok0 of the call. True if
+// a position was outside the table. Where every lane's two blocks share an axis (one axis, or
+// sections of even length) and every position is inside, a row takes one 16-byte load of angles
+// per lane and no checks, 16 rows in flight; with two 8-byte loads and checks per row the rotation
+// took 40 us of 131072 tokens x 2 heads, for its instructions more than its latency.
 template <int DT>
 __device__ __forceinline__ bool rotate_tile(uint32_t* tile, const RopeArgs& r, int64_t tok0, int r_lo, int r_hi, int lane) {
   using Q = QTile<DT>;
   RowPositions pos;
   pos.load(r, tok0 + lane - r_lo, lane >= r_lo && lane < r_hi, lane);
-  bool bad = false;
-  constexpr int kAhead = 16;
+  bool off = false;
+#pragma unroll
+  for (int a = 0; a < 4; ++a) off |= a < r.n_axes && static_cast<unsigned>(pos.p[a]) >= static_cast<unsigned>(r.n_positions);
+  if (__all_sync(0xffffffffu, !off && pos.a0 == pos.a1)) {
+    constexpr int kAhead = 16;
+    const float4* table = reinterpret_cast<const float4*>(r.table) + lane;
+#pragma unroll 1
+    for (int row = r_lo; row < r_hi; row += kAhead) {
+      float4 c[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) c[u] = __ldg(table + static_cast<int64_t>(pos.of(r, min(row + u, r_hi - 1)).x) * (kH / 2));
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (row + u >= r_hi) break;
+        rotate_row<DT>(tile + (row + u) * Q::kPitch, make_float2(c[u].x, c[u].y), make_float2(c[u].z, c[u].w), lane);
+      }
+    }
+    return false;
+  }
+  constexpr int kAhead = 4;
+#pragma unroll 1
   for (int row = r_lo; row < r_hi; row += kAhead) {
     float2 c0[kAhead], c1[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int2 q = pos.of(r, min(row + u, r_hi - 1));
-      bad |= outside(r, q);
       c0[u] = rope_cs(r, q.x, 2 * lane);
       c1[u] = rope_cs(r, q.y, 2 * lane + 1);
     }
@@ -122,7 +142,7 @@ __device__ __forceinline__ bool rotate_tile(uint32_t* tile, const RopeArgs& r, i
       rotate_row<DT>(tile + (row + u) * Q::kPitch, c0[u], c1[u], lane);
     }
   }
-  return bad;
+  return off;
 }
 
 // ---------------------------------------------------------------- tiles that get few tokens
