@@ -48,6 +48,7 @@ struct PagedAttn {
   unsigned* status;
   uint32_t wait_limit;
   int debug_no_loads;
+  int after_prefix;                       // the previous grid is the same call's prefix kernel: see the kernel
 };
 
 struct PgHeader {
@@ -106,9 +107,13 @@ __device__ __forceinline__ int pg_worker_of(int x, int chunks, int workers) {
   return static_cast<int>(((static_cast<long long>(x) + 1) * workers - 1) / chunks);
 }
 
-// Shares the batch out: chunk offsets of the sequences to `cs` (batch + 1 entries). A length that
-// is negative or past the table counts as none and is recorded.
-__device__ __forceinline__ int pg_scan(const PagedAttn& a, PgHeader& S, int* cs, bool refuse) {
+// Shares the batch out: chunk offsets of the sequences to `cs` (batch + 1 entries); `len` is that of
+// sequence threadIdx.x, loaded ahead. A length that is negative or past the table counts as none
+// and is recorded.
+struct PgScan {
+  int at, n;                              // of sequence threadIdx.x: first chunk, chunks (-1: refused)
+};
+__device__ __forceinline__ int pg_scan(const PagedAttn& a, PgHeader& S, int* cs, int len, PgScan& mine) {
   const int n = a.pg.batch;
   const long long room = static_cast<long long>(a.pg.max_pages) * a.pg.page_tiles * kTile;
   int sum = 0;
@@ -117,17 +122,16 @@ __device__ __forceinline__ int pg_scan(const PagedAttn& a, PgHeader& S, int* cs,
     int c = 0;
     bool ok = true;
     if (b < n) {
-      const int len = __ldg(a.pg.seq_lens + b);
+      if (b0 > 0) len = __ldg(a.pg.seq_lens + b);
       ok = len >= 0 && len <= room;
       if (ok) c = (len + kChunkTokens - 1) / kChunkTokens;
       else record_status(a.status, KVQ_ERR_RANGE);
     }
     int total;
     const int at = sum + block_exclusive(c, S.scan, kDecThreads / 32, total);
-    if (b < n) {
-      cs[b] = at;
-      if (blockIdx.x == 0) a.plan[b] = make_int2(at, (ok && !refuse) ? c : -1);
-    }
+    if (b < n) cs[b] = at;
+    if (b0 == 0) mine = PgScan{at, ok ? c : -1};
+    else if (b < n && blockIdx.x == 0) a.plan[b] = make_int2(at, ok ? c : -1);
     sum += total;
   }
   if (threadIdx.x == 0) {
@@ -182,8 +186,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
     reinterpret_cast<uint4*>(sm + kPgQOff)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (tid < kH) S.col_of[tid] = -1;
   __syncthreads();
-  grid_dependency_wait();
+  // Behind the same call's prefix kernel this grid starts as soon as that one's CTAs run: they have
+  // waited for everything before the call, and nothing here depends on the prefix. The merge does, and
+  // waits for this grid alone, so this one waits for the prefix kernel before it ends.
+  if (!a.after_prefix) grid_dependency_wait();
   // ------------------------------------------------------------------ header, slots, the batch
+  const int len0 = tid < a.pg.batch ? __ldg(a.pg.seq_lens + tid) : 0;
   if (warp == 0) {
     const int k_cols = min(max(al->plan_k_cols, 8), 96) & ~7;
     const bool ok = k_slots(al->plan_slot, k_cols, kD * a.pg.bits_k, S.slots);
@@ -211,12 +219,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
       record_status(a.status, code);
     }
   }
-  __syncthreads();
-  const int chunks = pg_scan(a, S, cs, S.bad != 0);
+  PgScan mine;
+  const int chunks = pg_scan(a, S, cs, len0, mine);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const bool bad = S.bad != 0;
+  if (blockIdx.x == 0 && tid < a.pg.batch) a.plan[tid] = make_int2(mine.at, bad ? -1 : mine.n);
   const uint32_t tbase = S.tmem_base + 128u * g;            // K-hat 96 (V-hat^T in 64 of them), S 16, O 16
   const uint32_t tS = tbase + 96, tO = tbase + 112;
   const int workers = pg_workers(chunks, a.ctas);
@@ -640,6 +649,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
   __syncthreads();
   tc::fence_after_sync();
   if (warp == kDecIssuerWarp0) tc::tmem_dealloc(S.tmem_base, kTmemCols);
+  if (a.after_prefix) grid_dependency_wait();
 }
 
 // ---------------------------------------------------------------- merge

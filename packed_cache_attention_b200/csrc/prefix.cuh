@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
   if (is_issuer) tc::tmem_alloc(&S.tmem_base, kTmemCols);
   __syncthreads();
   grid_dependency_wait();
+  allow_dependents();                                       // the call's own-pages kernel may fill the other SMs
   if (warp == 0) {
     const int k_cols = min(max(al->plan_k_cols, 8), 96) & ~7;
     const bool ok = k_slots(al->plan_slot, k_cols, kD * a.pg.bits_k, S.slots);
@@ -465,7 +466,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
     }
   }
   __syncthreads();
-  allow_dependents();
   const bool aborted = bad || S.bad_page != 0 || S.abort != 0;
   if (tid == 0) {
     // (the table's copy lands before the CTA leaves, used or not)

@@ -79,15 +79,13 @@ __global__ void __launch_bounds__(kRopeThreads) kvq_rope_rows(const RopeRows a, 
   const int64_t tok = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / LPR) + threadIdx.x / LPR;
   if (tok < a.n_tokens) {
     const int b0 = V * (threadIdx.x % LPR);
-    float2 cs[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) cs[i] = rope_cs(r, r.positions[r.axis[b0 + i] * r.axis_stride + tok], b0 + i);
     const int64_t b = tok / a.seq_len, t = tok % a.seq_len;
     const int h0 = blockIdx.y * a.heads_per_cta, h1 = min(a.n_heads, h0 + a.heads_per_cta);
     const uint8_t* xp = a.x + ES * (b * a.xsb + t * a.xst + b0);
     uint8_t* op = a.out + ES * (b * a.osb + t * a.ost + b0);
-    for (int h = h0; h < h1; h += kRopeBatch) {
-      uint4 lo[kRopeBatch], hi[kRopeBatch];
+    // the first rows are on their way before the positions are looked at
+    uint4 lo[kRopeBatch], hi[kRopeBatch];
+    auto load = [&](int h) {
 #pragma unroll
       for (int u = 0; u < kRopeBatch; ++u) {
         if (h + u < h1) {
@@ -96,6 +94,12 @@ __global__ void __launch_bounds__(kRopeThreads) kvq_rope_rows(const RopeRows a, 
           hi[u] = *reinterpret_cast<const uint4*>(p + ES * kH);
         }
       }
+    };
+    load(h0);
+    float2 cs[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) cs[i] = rope_cs(r, r.positions[r.axis[b0 + i] * r.axis_stride + tok], b0 + i);
+    for (int h = h0; h < h1; h += kRopeBatch) {
 #pragma unroll
       for (int u = 0; u < kRopeBatch; ++u) {
         if (h + u >= h1) break;
@@ -120,6 +124,7 @@ __global__ void __launch_bounds__(kRopeThreads) kvq_rope_rows(const RopeRows a, 
         *reinterpret_cast<uint4*>(p) = make_uint4(l[0], l[1], l[2], l[3]);
         *reinterpret_cast<uint4*>(p + ES * kH) = make_uint4(g[0], g[1], g[2], g[3]);
       }
+      if (h + kRopeBatch < h1) load(h + kRopeBatch);
     }
   }
   allow_dependents();

@@ -616,7 +616,8 @@ def kvq_paged_decode_attn(q, pool, alloc, desc: PagedDesc, block_table, seq_lens
     B, Hq, d = q.shape
     dev = _on_device(q, pool, alloc, block_table, seq_lens, prefix_pages, out, ws)
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=torch.float32 if out_dtype is None else out_dtype, device=q.device)
+        out = torch.empty_like(q, dtype=torch.float32 if out_dtype is None else out_dtype,
+                               memory_format=torch.contiguous_format)
     elif out.shape != q.shape or not out.is_contiguous() or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be contiguous, of q's shape and of out_dtype")
     if ws is None:
