@@ -4,7 +4,8 @@
 // the same keys and values, so a chunk of 128 tokens is dequantized once for up to 128 rows:
 //   S[128 rows][128 tokens] = Q' x Khat^T,   O[128 rows][128 dims] += P' x Vhat
 // with tcgen05.mma (M 128, N 128). lane = row in the softmax: a row's maximum and sum are a
-// thread's own values, and the four warpgroups take 32 tokens each of the same rows.
+// thread's own values. Two warpgroups look Khat and Vhat up (shared-memory loads and integer
+// operations), two run the softmax (exponentials, fp32), 64 tokens each of the same rows.
 //
 // Precision: Q' and P' are fp16 high + low parts (Khat and Vhat are fp16 centroids, exact), so every
 // product runs twice; the norms of keys and values multiply the fp32 logits and shares. A
@@ -17,9 +18,10 @@
 // rows x 16 bytes contiguous, 2048 bytes per 8 K elements, so a lookup's 4 words (8 elements
 // of a token's key, or 8 tokens of a dim) are one 16-byte store next to its neighbour lane's.
 //
-// Order within chunk j: Khat of chunk j + 1 is looked up and S(j + 1) issued before the softmax of
-// chunk j, V-hat of chunk j after it; so S runs under the softmax and O under the next chunk's
-// keys. 12.9k cycles a chunk with tokens as lanes (its row maxima need a warp reduction per row).
+// Order: the producers write Khat(j + 1) once S(j) is done and Vhat(j) once O(j - 1) is; S(j + 1) is
+// issued before O(j), into the other buffer, so it runs under the softmax of chunk j. With all
+// warps taking every step in turn a chunk took 5.9k cycles; with tokens as lanes, whose row maxima
+// need a warp reduction per row, 12.9k.
 //
 // Every wait is bounded, as in kvq_decode_gtq; a CTA that gave up, or met a bad header or page,
 // leaves NaN maxima, at which the merge leaves the rows as they are.
@@ -52,15 +54,15 @@ struct PrefixArgs {
 
 struct PreHeader {
   uint64_t fullk[kPgStagesMax], fullv[kPgStagesMax];
-  uint64_t kready, sfull, vready, ofull, drain, setup;
+  uint64_t kready, sfull[2], vready, ofull, drain, setup;   // sfull by chunk parity: see the consumers
   uint32_t tmem_base;
   int bad, bad_page, abort;
   int k_cols;
   KSlots slots;
   alignas(16) float dequant[kH];
   int8_t col_block[96];
-  alignas(16) float norm[2][2][kChunkTokens];   // [chunk parity][key, value / sqrt(d)][token]
-  float xch[2][4][kPreRows];                    // [chunk parity][warpgroup][row]: maximum; sums at the end
+  alignas(16) float norm[4][2][kChunkTokens];   // [chunk mod 4][key, value / sqrt(d)][token]
+  float xch[2][4][kPreRows];                    // [chunk parity][softmax warpgroup][row]: maximum; sums at the end
 };
 
 // Shared memory: header, Q' low of the first kPreQCut K steps; lookup tables (at their address); Q'
@@ -114,8 +116,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
       tc::mbar_init(&S.fullk[s], 1);
       tc::mbar_init(&S.fullv[s], 1);
     }
-    tc::mbar_init(&S.kready, 16);
-    tc::mbar_init(&S.sfull, 1);
+    tc::mbar_init(&S.kready, 8);
+    tc::mbar_init(&S.sfull[0], 2);
+    tc::mbar_init(&S.sfull[1], 2);
     tc::mbar_init(&S.vready, 16);
     tc::mbar_init(&S.ofull, 1);
     tc::mbar_init(&S.drain, 1);
@@ -225,7 +228,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
           tc::mma_ts(d, tb + 8 * ks, tc::sdesc(bk + 4096 * ks, 2048, 128), id, ks > 0 ? 1u : 0u);
         for (int ks = 0; ks < k_steps; ++ks)
           tc::mma_ss(d, tc::sdesc(smb + pre_q_step(ks), 2048, 128), tc::sdesc(bk + 4096 * ks, 2048, 128), id, 1u);
-        tc::mma_commit(&S.sfull);
+        tc::mma_commit(&S.sfull[j & 1]);
+        tc::mbar_arrive(&S.sfull[j & 1]);                   // (passes on the producers' norms)
       }
       __syncwarp();
       if (nk < n && loads) copy_k();
@@ -313,159 +317,188 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
       *reinterpret_cast<uint4*>(p + 2048) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
     }
     tc::wait_st();
+    tc::fence_proxy_async_smem();                           // Q' low, before anyone's kready
+    tc::fence_before_sync();
     named_sync(1, 512);                                     // the staged rows are read
     if (!tc::mbar_wait(&S.setup, 0, WL)) *abort_flag = 1;
 
-    // Khat(j) and the norms of its tokens (lane = token; a warpgroup takes every fourth slot)
-    Ring rk, rv;
-    auto keys = [&](int j) {
-      const int s = rk.s;
-      if (!tc::mbar_wait(&S.fullk[s], rk.parity, WL)) *abort_flag = 1;
-      rk.next(NS);
-      const uint8_t* rec = stages + static_cast<size_t>(s) * cbytes + q * kbytes;
-      const uint8_t* kw = rec + lane4;
-      k_lookup(kw, S.slots, wg, kPlanSlots, 4, lane4, [&](int slot, const uint32_t (&v)[4]) {
-        *reinterpret_cast<uint4*>(sm + kPreKOff + slot * 2048 + t * 16) = make_uint4(v[0], v[1], v[2], v[3]);
-      });
-      if (wg == (j & 3)) {
-        const bool valid = (c_begin + j) * kChunkTokens + t < a.len;
-        const uint16_t* nrm = reinterpret_cast<const uint16_t*>(rec + 4 * kD * a.pg.bits_k) + lane;
-        S.norm[j & 1][0][t] = valid ? __half2float(__ushort_as_half(nrm[0])) : 0.0f;
-        S.norm[j & 1][1][t] = valid ? __half2float(__ushort_as_half(nrm[kTile])) * (inv_sqrt_d * kPgScale) : 0.0f;
-      }
-      tc::fence_proxy_async_smem();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&S.kready);
-    };
-    keys(0);
-    named_sync(1, 512);                                     // the first norms
-    const uint32_t tO = tb + kPreO + lane_base + 32 * wg;
-    bool stopped = false;
-    for (int j = 0; j < n; ++j) {
-      if (!tc::mbar_wait(&S.sfull, j & 1, WL)) *abort_flag = 1;
-      tc::fence_after_sync();
-      if (j + 1 < n) keys(j + 1);
-      // ------------------------------------------------------------ logits (lane = row, 32 tokens)
-      const uint32_t tS = tb + kPreS + 128u * (j & 1) + lane_base + 32 * wg;
-      float x[32];
-      float top = -INFINITY;
-      if (live) {
-        uint32_t sr[32];
-        tc::tmem_ld<16>(tS, *reinterpret_cast<uint32_t(*)[16]>(sr));
-        tc::tmem_ld<16>(tS + 16, *reinterpret_cast<uint32_t(*)[16]>(sr + 16));
-        tc::wait_ld();
-        const float4* kn = reinterpret_cast<const float4*>(S.norm[j & 1][0] + 32 * wg);
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 f = kn[i >> 2];
-          const float2 u = mul2(make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), make_float2(f.x, f.y));
-          const float2 v = mul2(make_float2(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])), make_float2(f.z, f.w));
-          x[i] = u.x; x[i + 1] = u.y; x[i + 2] = v.x; x[i + 3] = v.y;
+    if (wg < 2) {
+      // ---------------------------------------------------------------- producers: Khat and Vhat
+      Ring rk, rv;
+      // Khat(j) and the norms of its tokens (lane = token; a warpgroup takes every second slot)
+      auto keys = [&](int j) {
+        const int s = rk.s;
+        if (!tc::mbar_wait(&S.fullk[s], rk.parity, WL)) *abort_flag = 1;
+        rk.next(NS);
+        const uint8_t* rec = stages + static_cast<size_t>(s) * cbytes + q * kbytes;
+        k_lookup(rec + lane4, S.slots, wg, kPlanSlots, 2, lane4, [&](int slot, const uint32_t (&v)[4]) {
+          *reinterpret_cast<uint4*>(sm + kPreKOff + slot * 2048 + t * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+        });
+        if (wg == (j & 1)) {
+          const bool valid = (c_begin + j) * kChunkTokens + t < a.len;
+          const uint16_t* nrm = reinterpret_cast<const uint16_t*>(rec + 4 * kD * a.pg.bits_k) + lane;
+          S.norm[j & 3][0][t] = valid ? __half2float(__ushort_as_half(nrm[0])) : 0.0f;
+          S.norm[j & 3][1][t] = valid ? __half2float(__ushort_as_half(nrm[kTile])) * (inv_sqrt_d * kPgScale) : 0.0f;
         }
-        const int left = a.len - (c_begin + j) * kChunkTokens - 32 * wg;   // tokens of the prefix from this one on
-        if (left < 32) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = i < left ? x[i] : -INFINITY;
+        tc::fence_proxy_async_smem();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&S.kready);
+      };
+      keys(0);
+      for (int j = 0; j < n && *abort_flag == 0; ++j) {
+        if (j + 1 < n) {
+          if (!tc::mbar_wait(&S.sfull[j & 1], (j >> 1) & 1, WL)) *abort_flag = 1;   // Khat(j) is read
+          keys(j + 1);
         }
-        float m4[4] = {x[0], x[1], x[2], x[3]};
+        // Vhat(j) (lane = dim; a warpgroup takes two tiles)
+        if (!tc::mbar_wait(&S.fullv[rv.s], rv.parity, WL)) *abort_flag = 1;
+        const uint8_t* sv = stages + static_cast<size_t>(rv.s) * cbytes + kChunkTiles * kbytes;
+        rv.next(NS);
 #pragma unroll
-        for (int i = 4; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
-        top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qs;
+        for (int u = 0; u < 2; ++u) {
+          uint32_t v16[16];
+          v_vals_any(a.pg.bits_v, reinterpret_cast<const uint32_t*>(sv + (wg + 2 * u) * vbytes) + t, tab, v16);
+          if (u == 0 && j > 0 && !tc::mbar_wait(&S.ofull, (j - 1) & 1, WL)) *abort_flag = 1;   // Vhat(j - 1) is read
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(sm + kPreVOff + (4 * (wg + 2 * u) + i) * 2048 + t * 16) =
+                make_uint4(v16[4 * i], v16[4 * i + 1], v16[4 * i + 2], v16[4 * i + 3]);
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&S.vready);
       }
-      S.xch[j & 1][wg][t] = top;
-      // a wait that gave up joins the barrier's vote, so that the warps stop as one
-      if (named_sync_or(1, 512, *abort_flag != 0)) {
-        stopped = true;
-        break;
-      }
-      if (live) {
-        const float (*xc)[kPreRows] = S.xch[j & 1];
-        const float cm = fmaxf(fmaxf(xc[0][t], xc[1][t]), fmaxf(xc[2][t], xc[3][t]));
-        const bool up = cm > M + static_cast<float>(kPgThr);
-        if (__any_sync(0xffffffffu, up)) {
-          const float mn = up ? cm : M;
-          const float alpha = (M == -INFINITY) ? 0.0f : fast_exp2(M - mn);
-          M = mn;
-          L *= alpha;
-          if (j > 0) {                                      // O holds earlier chunks
-            if (!tc::mbar_wait(&S.ofull, (j - 1) & 1, WL)) *abort_flag = 1;
-            tc::fence_after_sync();
-            const float2 al2 = make_float2(alpha, alpha);
+    } else {
+      // ---------------------------------------------------------------- consumers: softmax (lane = row)
+      const int cw = wg - 2;                                // tokens 64 cw .. 64 cw + 63
+      const uint32_t tO = tb + kPreO + lane_base + 64 * cw;
+      bool stopped = false;
+      for (int j = 0; j < n; ++j) {
+        // S(j + 1) may be done before a warp that lags gets here, S(j + 2) not (it needs O(j)): two
+        // barriers tell their phases apart
+        if (!tc::mbar_wait(&S.sfull[j & 1], (j >> 1) & 1, WL)) *abort_flag = 1;
+        tc::fence_after_sync();
+        const uint32_t tS = tb + kPreS + 128u * (j & 1) + lane_base + 64 * cw;
+        const float4* kn = reinterpret_cast<const float4*>(S.norm[j & 3][0] + 64 * cw);
+        const float4* vn = reinterpret_cast<const float4*>(S.norm[j & 3][1] + 64 * cw);
+        const int left = a.len - (c_begin + j) * kChunkTokens - 64 * cw;   // tokens of the prefix from the first one on
+        // logits over 2^e: S times the keys' norms, -inf past the prefix
+        auto logits = [&](int c0, float (&x)[16]) {
+          uint32_t sr[16];
+          tc::tmem_ld<16>(tS + c0, sr);
+          tc::wait_ld();
 #pragma unroll
-            for (int c0 = 0; c0 < 32; c0 += 16) {
-              uint32_t o[16];
-              tc::tmem_ld<16>(tO + c0, o);
-              tc::wait_ld();
+          for (int i = 0; i < 16; i += 4) {
+            const float4 f = kn[(c0 + i) >> 2];
+            const float2 u = mul2(make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), make_float2(f.x, f.y));
+            const float2 v = mul2(make_float2(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])), make_float2(f.z, f.w));
+            x[i] = u.x; x[i + 1] = u.y; x[i + 2] = v.x; x[i + 3] = v.y;
+          }
+          if (left < 64) {
 #pragma unroll
-              for (int c = 0; c < 16; c += 2) {
-                const float2 y = mul2(make_float2(__uint_as_float(o[c]), __uint_as_float(o[c + 1])), al2);
-                o[c] = __float_as_uint(y.x);
-                o[c + 1] = __float_as_uint(y.y);
+            for (int i = 0; i < 16; ++i) x[i] = c0 + i < left ? x[i] : -INFINITY;
+          }
+        };
+        float top = -INFINITY;
+        if (live) {
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c0 = 0; c0 < 64; c0 += 16) {
+            float x[16];
+            logits(c0, x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
+          }
+          top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qs;
+        }
+        S.xch[j & 1][cw][t] = top;
+        // a wait that gave up joins the barrier's vote, so that the warps stop as one
+        if (named_sync_or(2, 256, *abort_flag != 0)) {
+          stopped = true;
+          break;
+        }
+        if (live) {
+          const float cm = fmaxf(S.xch[j & 1][0][t], S.xch[j & 1][1][t]);
+          const bool up = cm > M + static_cast<float>(kPgThr);
+          if (__any_sync(0xffffffffu, up)) {
+            const float mn = up ? cm : M;
+            const float alpha = (M == -INFINITY) ? 0.0f : fast_exp2(M - mn);
+            M = mn;
+            L *= alpha;
+            if (j > 0) {                                    // O holds earlier chunks
+              if (!tc::mbar_wait(&S.ofull, (j - 1) & 1, WL)) *abort_flag = 1;
+              tc::fence_after_sync();
+              const float2 al2 = make_float2(alpha, alpha);
+#pragma unroll
+              for (int c0 = 0; c0 < 64; c0 += 16) {
+                uint32_t o[16];
+                tc::tmem_ld<16>(tO + c0, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int c = 0; c < 16; c += 2) {
+                  const float2 y = mul2(make_float2(__uint_as_float(o[c]), __uint_as_float(o[c + 1])), al2);
+                  o[c] = __float_as_uint(y.x);
+                  o[c + 1] = __float_as_uint(y.y);
+                }
+                tc::tmem_st<16>(tO + c0, o);
               }
-              tc::tmem_st<16>(tO + c0, o);
             }
           }
-        }
-        // ---------------------------------------------------------- P', over the S columns just read
-        const float2 qs2 = make_float2(qs, qs), nM = make_float2(-M, -M);
-        const float4* vn = reinterpret_cast<const float4*>(S.norm[j & 1][1] + 32 * wg);
-        float2 sum = make_float2(0.0f, 0.0f);
-        uint32_t hi[16];
+          // P' of 32 tokens at a time, over the S columns just read
+          const float2 qs2 = make_float2(qs, qs), nM = make_float2(-M, -M);
+          float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 f = vn[i >> 2];
+          for (int g0 = 0; g0 < 64; g0 += 32) {
+            float x[2][16];
+            logits(g0, x[0]);
+            logits(g0 + 16, x[1]);
+            uint32_t hi[16];
 #pragma unroll
-          for (int k = i; k < i + 4; k += 2) {
-            const float2 z = fma2(make_float2(x[k], x[k + 1]), qs2, nM);
-            const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
-            sum = add2(sum, p);
-            const float2 y = mul2(p, k == i ? make_float2(f.x, f.y) : make_float2(f.z, f.w));
-            const __half2 yh = __floats2half2_rn(y.x, y.y);
-            hi[k >> 1] = *reinterpret_cast<const uint32_t*>(&yh);
-            x[k] = y.x;
-            x[k + 1] = y.y;
+            for (int i = 0; i < 32; i += 4) {
+              const float4 f = vn[(g0 + i) >> 2];
+#pragma unroll
+              for (int k = i; k < i + 4; k += 2) {
+                float* xx = &x[k >> 4][k & 15];
+                const float2 z = fma2(make_float2(xx[0], xx[1]), qs2, nM);
+                const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+                sum = add2(sum, p);
+                const float2 y = mul2(p, k == i ? make_float2(f.x, f.y) : make_float2(f.z, f.w));
+                const __half2 yh = __floats2half2_rn(y.x, y.y);
+                hi[k >> 1] = *reinterpret_cast<const uint32_t*>(&yh);
+                xx[0] = y.x;
+                xx[1] = y.y;
+              }
+            }
+            tc::tmem_st<16>(tS + g0, hi);
+            if (a.low_p) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const float* xx = &x[k >> 4][k & 15];
+                const float2 r = fma2(__half22float2(*reinterpret_cast<const __half2*>(&hi[k >> 1])), make_float2(-1.0f, -1.0f),
+                                      make_float2(xx[0], xx[1]));
+                const __half2 yl = __floats2half2_rn(r.x, r.y);
+                hi[k >> 1] = *reinterpret_cast<const uint32_t*>(&yl);
+              }
+              tc::tmem_st<16>(tS + g0 + 16, hi);
+            }
           }
+          L += sum.x + sum.y;
         }
-        tc::tmem_st<16>(tS, hi);
-        if (a.low_p) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            const float2 r = fma2(__half22float2(*reinterpret_cast<const __half2*>(&hi[k >> 1])), make_float2(-1.0f, -1.0f),
-                                  make_float2(x[k], x[k + 1]));
-            const __half2 yl = __floats2half2_rn(r.x, r.y);
-            hi[k >> 1] = *reinterpret_cast<const uint32_t*>(&yl);
-          }
-          tc::tmem_st<16>(tS + 16, hi);
-        }
-        L += sum.x + sum.y;
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&S.vready);
       }
-      // ------------------------------------------------------------ values (lane = dim, one tile a warpgroup)
-      const int s = rv.s;
-      if (!tc::mbar_wait(&S.fullv[s], rv.parity, WL)) *abort_flag = 1;
-      rv.next(NS);
-      uint32_t v16[16];
-      v_vals_any(a.pg.bits_v,
-                 reinterpret_cast<const uint32_t*>(stages + static_cast<size_t>(s) * cbytes + kChunkTiles * kbytes + wg * vbytes) + t,
-                 tab, v16);
-      if (j > 0 && !tc::mbar_wait(&S.ofull, (j - 1) & 1, WL)) *abort_flag = 1;   // Vhat of the last chunk is read
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4*>(sm + kPreVOff + (4 * wg + i) * 2048 + t * 16) =
-            make_uint4(v16[4 * i], v16[4 * i + 1], v16[4 * i + 2], v16[4 * i + 3]);
-      tc::fence_proxy_async_smem();
-      tc::wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&S.vready);
-    }
-    if (!stopped) {
-      if (!tc::mbar_wait(&S.ofull, (n - 1) & 1, WL)) *abort_flag = 1;
-      tc::fence_after_sync();
-      S.xch[n & 1][wg][t] = L;
+      if (!stopped) {
+        if (!tc::mbar_wait(&S.ofull, (n - 1) & 1, WL)) *abort_flag = 1;
+        tc::fence_after_sync();
+        S.xch[n & 1][cw][t] = L;
+      }
     }
   }
   __syncthreads();
+  tc::fence_after_sync();
   const bool aborted = bad || S.bad_page != 0 || S.abort != 0;
   if (tid == 0) {
     // (the table's copy lands before the CTA leaves, used or not)
@@ -475,10 +508,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
   if (!is_issuer) {
     const int t = 32 * q + lane;
     const size_t i = static_cast<size_t>(blockIdx.x) * kPreRows + t;
-    if (wg == 0 && t < rows) {
+    if (wg == 2 && t < rows) {
       const float (*xc)[kPreRows] = S.xch[n & 1];
       a.part_m[i] = aborted ? __int_as_float(0x7fc00000) : M;
-      a.part_l[i] = aborted ? 0.0f : (xc[0][t] + xc[1][t]) + (xc[2][t] + xc[3][t]);
+      a.part_l[i] = aborted ? 0.0f : xc[0][t] + xc[1][t];
     }
     if (!aborted && 32 * q < rows) {
       float4* po = reinterpret_cast<float4*>(a.part_o + i * kD + 32 * wg);
