@@ -1079,7 +1079,7 @@ PagedWs paged_ws(int batch, int n_kv_heads, int group, bool prefix) {
   return w;
 }
 
-kvq_status launch_prefix(PrefixArgs a, cudaStream_t s) {
+kvq_status launch_prefix(PrefixArgs a, int splits, cudaStream_t s) {
   static SmemOptIn opt;
   const size_t cb = chunk_bytes(a.pg.rec_bytes), room = max_smem() - kPreStageOff;
   a.n_stages = static_cast<int>(std::min<size_t>(kPgStagesMax, room / cb));
@@ -1087,7 +1087,7 @@ kvq_status launch_prefix(PrefixArgs a, cudaStream_t s) {
   const size_t smem = kPreStageOff + a.n_stages * cb;
   const kvq_status st = opt.raise(kvq_prefix_gtq, smem);
   if (st != KVQ_OK) return st;
-  const unsigned grid = static_cast<unsigned>(a.splits * a.row_groups * a.pg.n_kv_heads);
+  const unsigned grid = static_cast<unsigned>(splits * a.row_groups * a.pg.n_kv_heads);
   const cudaError_t e = launch_pdl(kvq_prefix_gtq, dim3(grid), dim3(kPreThreads), smem, s, a);
   return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
 }
@@ -1259,7 +1259,8 @@ kvq_status kvq_paged_decode_attn(const void* q, const kvq_tensor4* qd, const voi
   m.own_o = reinterpret_cast<const float*>(w8 + w.own_o);
   if (plen > 0) {
     PrefixPlan pp = prefix_plan(seqs->batch * group, d->n_kv_heads);
-    pp.splits = std::min(pp.splits, (n_tiles_of(plen) + kChunkTiles - 1) / kChunkTiles);
+    const int chunks = (n_tiles_of(plen) + kChunkTiles - 1) / kChunkTiles, per = (chunks + pp.splits - 1) / pp.splits;
+    pp.splits = (chunks + per - 1) / per;
     PrefixArgs a{};
     a.q = q;
     a.qsb = qd->stride_b;
@@ -1272,7 +1273,7 @@ kvq_status kvq_paged_decode_attn(const void* q, const kvq_tensor4* qd, const voi
     a.pg = pg;
     a.pages = prefix->pages;
     a.len = plen;
-    a.splits = pp.splits;
+    a.per = per;
     a.row_groups = pp.groups;
     a.low_p = out_dtype != KVQ_BF16;
     a.part_m = reinterpret_cast<float*>(w8 + w.pre_m);
@@ -1281,7 +1282,7 @@ kvq_status kvq_paged_decode_attn(const void* q, const kvq_tensor4* qd, const voi
     a.status = reinterpret_cast<unsigned*>(w8);
     a.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
     a.debug_no_loads = g_debug_no_loads.load(std::memory_order_relaxed);
-    if ((st = launch_prefix(a, s)) != KVQ_OK) return st;
+    if ((st = launch_prefix(a, pp.splits, s)) != KVQ_OK) return st;
     m.prefix_len = plen;
     m.pre_groups = pp.groups;
     m.pre_splits = pp.splits;

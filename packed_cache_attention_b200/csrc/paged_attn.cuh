@@ -92,23 +92,21 @@ struct Ring {
   }
 };
 
-// The 4 * ctas warpgroups of a head share `chunks` chunks: as few as keep the longest range.
-__device__ __forceinline__ int pg_workers(int chunks, int ctas) {
-  const int per = max(1, (chunks + 4 * ctas - 1) / (4 * ctas));
-  return (chunks + per - 1) / per;
-}
-__device__ __forceinline__ int pg_first_chunk(int w, int chunks, int workers) {
-  return static_cast<int>(static_cast<long long>(w) * chunks / workers);
-}
-// A CTA's warpgroups take consecutive ranges, as few of them as the workers need.
-__device__ __forceinline__ int pg_per_cta(int workers, int ctas) { return max(1, (workers + ctas - 1) / ctas); }
-// The warpgroup whose range holds chunk x.
-__device__ __forceinline__ int pg_worker_of(int x, int chunks, int workers) {
-  return static_cast<int>(((static_cast<long long>(x) + 1) * workers - 1) / chunks);
-}
+// The 4 * ctas warpgroups of a head share `chunks` chunks, `per` each (the last one what is left):
+// as few as keep the longest range. (32-bit divisions: 64-bit ones took 1 us of a call.)
+struct Shares {
+  int per, workers, per_cta, chunks;        // chunks of a worker, workers, workers of a CTA (consecutive ranges)
+  __device__ __forceinline__ Shares(int chunks, int ctas) : chunks(chunks) {
+    per = max(1, (chunks + 4 * ctas - 1) / (4 * ctas));
+    workers = (chunks + per - 1) / per;
+    per_cta = max(1, (workers + ctas - 1) / ctas);
+  }
+  __device__ __forceinline__ int first(int w) const { return min(w * per, chunks); }   // first chunk of worker w
+  __device__ __forceinline__ int of(int x) const { return x / per; }                   // worker of chunk x
+};
 
 // Shares the batch out: chunk offsets of the sequences to `cs` (batch + 1 entries); `len` is that of
-// sequence threadIdx.x, loaded ahead. A length that is negative or past the table counts as none
+// sequence threadIdx.x (of the lane's for up to 32 sequences), loaded ahead. A length that is negative or past the table counts as none
 // and is recorded.
 struct PgScan {
   int at, n;                              // of sequence threadIdx.x: first chunk, chunks (-1: refused)
@@ -116,6 +114,28 @@ struct PgScan {
 __device__ __forceinline__ int pg_scan(const PagedAttn& a, PgHeader& S, int* cs, int len, PgScan& mine) {
   const int n = a.pg.batch;
   const long long room = static_cast<long long>(a.pg.max_pages) * a.pg.page_tiles * kTile;
+  if (n <= 32) {                          // a warp's scan, which every warp makes for itself
+    const int lane = threadIdx.x & 31;
+    const bool ok = len >= 0 && len <= room;
+    const int c = ok ? (len + kChunkTokens - 1) / kChunkTokens : 0;
+    int inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    const int sum = __shfl_sync(0xffffffffu, inc, 31);
+    if (threadIdx.x < n) {
+      if (!ok) record_status(a.status, KVQ_ERR_RANGE);
+      cs[lane] = inc - c;
+    }
+    mine = PgScan{inc - c, ok ? c : -1};
+    if (threadIdx.x == 0) {
+      cs[n] = sum;
+      if (blockIdx.x == 0) a.plan[n] = make_int2(sum, 0);
+    }
+    return sum;
+  }
   int sum = 0;
   for (int b0 = 0; b0 < n; b0 += kDecThreads) {
     const int b = b0 + threadIdx.x;
@@ -136,7 +156,7 @@ __device__ __forceinline__ int pg_scan(const PagedAttn& a, PgHeader& S, int* cs,
   }
   if (threadIdx.x == 0) {
     cs[n] = sum;
-    if (blockIdx.x == 0) a.plan[n] = make_int2(sum, pg_workers(sum, a.ctas));
+    if (blockIdx.x == 0) a.plan[n] = make_int2(sum, 0);
   }
   return sum;
 }
@@ -191,7 +211,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
   // waits for this grid alone, so this one waits for the prefix kernel before it ends.
   if (!a.after_prefix) grid_dependency_wait();
   // ------------------------------------------------------------------ header, slots, the batch
-  const int len0 = tid < a.pg.batch ? __ldg(a.pg.seq_lens + tid) : 0;
+  const int scan_i = a.pg.batch <= 32 ? lane : tid;
+  const int len0 = scan_i < a.pg.batch ? __ldg(a.pg.seq_lens + scan_i) : 0;
   if (warp == 0) {
     const int k_cols = min(max(al->plan_k_cols, 8), 96) & ~7;
     const bool ok = k_slots(al->plan_slot, k_cols, kD * a.pg.bits_k, S.slots);
@@ -228,16 +249,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
   if (blockIdx.x == 0 && tid < a.pg.batch) a.plan[tid] = make_int2(mine.at, bad ? -1 : mine.n);
   const uint32_t tbase = S.tmem_base + 128u * g;            // K-hat 96 (V-hat^T in 64 of them), S 16, O 16
   const uint32_t tS = tbase + 96, tO = tbase + 112;
-  const int workers = pg_workers(chunks, a.ctas);
-  const int per = pg_per_cta(workers, a.ctas);
-  const int w_cta = cta * per, w_end = min(w_cta + per, workers);   // this CTA's workers
-  const int w = g < per ? w_cta + g : workers;
-  const int x0 = w < workers ? pg_first_chunk(w, chunks, workers) : 0;
-  const int x1 = w < workers ? pg_first_chunk(w + 1, chunks, workers) : 0;
+  const Shares sh(chunks, a.ctas);
+  const int w_cta = cta * sh.per_cta, w_end = min(w_cta + sh.per_cta, sh.workers);   // this CTA's workers
+  const int w = g < sh.per_cta ? w_cta + g : sh.workers;
+  const int x0 = w < sh.workers ? sh.first(w) : 0, x1 = w < sh.workers ? sh.first(w + 1) : 0;
   const int b0 = x1 > x0 ? find_span(cs, a.pg.batch, x0) : 0;
   // several workers inside one sequence leave one share, at the first one's entry
-  const bool joint = w_cta + 1 < w_end && pg_first_chunk(w_end, chunks, workers) <=
-                                              cs[find_span(cs, a.pg.batch, pg_first_chunk(w_cta, chunks, workers)) + 1];
+  const int b_cta = w_cta + 1 < w_end ? find_span(cs, a.pg.batch, sh.first(w_cta)) : 0;
+  const bool joint = w_cta + 1 < w_end && sh.first(w_end) <= cs[b_cta + 1];
   volatile int* abort_flag = &S.wg_abort[g];
   const size_t e0 = static_cast<size_t>(hkv) * a.entries + w;   // entry of sequence b: e0 + b
 
@@ -440,10 +459,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
         const uint8_t* kw = st + q * kbytes + lane4;
         auto put = [&](int slot, const uint32_t (&v)[4]) { tc::tmem_st<4>(tbase + lane_base + 4 * slot, v); };
         // the first columns are free already, the others held the last chunk's V-hat^T
-        k_lookup(kw, S.slots, 0, kPgVCol / 4, 1, lane4, put);
+        k_lookup<2>(kw, S.slots, 0, kPgVCol / 4, 1, lane4, put);
         if (j > 0 && !tc::mbar_wait(&S.ofull[g], (j - 1) & 1, WL)) *abort_flag = 1;
         tc::fence_after_sync();
-        k_lookup(kw, S.slots, kPgVCol / 4, kPlanSlots, 1, lane4, put);
+        k_lookup<2>(kw, S.slots, kPgVCol / 4, kPlanSlots, 1, lane4, put);
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
@@ -559,13 +578,26 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
         uint32_t o[16];
         tc::tmem_ld<16>(tO + lane_base, o);
         tc::wait_ld();
+        // Row sums over the warp: at each step a lane keeps half of its rows and passes on the others;
+        // lane l ends with row l / (32 / kRows).
         float l[kRows];
 #pragma unroll
-        for (int h = 0; h < kRows; ++h) {
-          l[h] = (h & 1) ? L[h >> 1].y : L[h >> 1].x;
+        for (int h = 0; h < kRows; ++h) l[h] = (h & 1) ? L[h >> 1].y : L[h >> 1].x;
 #pragma unroll
-          for (int k = 16; k > 0; k >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], k);
+        for (int k = 16, nr = kRows / 2; k > 0; k >>= 1, nr >>= 1) {
+          if (nr > 0) {
+            const bool up = (lane & k) != 0;
+#pragma unroll
+            for (int h = 0; h < nr; ++h) {
+              const float give = up ? l[h] : l[h + nr], keep = up ? l[h + nr] : l[h];
+              l[h] = keep + __shfl_xor_sync(0xffffffffu, give, k);
+            }
+          } else {
+            l[0] += __shfl_xor_sync(0xffffffffu, l[0], k);
+          }
         }
+        constexpr int kPer = 32 / kRows;
+        const int lr = lane / kPer;                         // the row whose sum this lane has
         const float gone = __int_as_float(0x7fc00000);
         if (joint) {
           // the stages are free now: every copy of this warpgroup has been read
@@ -573,22 +605,18 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
 #pragma unroll
           for (int h = 0; h < kRows; ++h) {
             po[h * kD] = __uint_as_float(o[h]) + __uint_as_float(o[8 + h]);
-            if (lane == 0) {
-              S.join_l[g][q][h] = l[h];
-              if (q == 0) S.join_m[g][h] = seg_bad ? gone : -((h & 1) ? nM[h >> 1].y : nM[h >> 1].x);
-            }
+            if (lane == 0 && q == 0) S.join_m[g][h] = seg_bad ? gone : -((h & 1) ? nM[h >> 1].y : nM[h >> 1].x);
           }
+          if (lane % kPer == 0) S.join_l[g][q][lr] = l[0];
         } else {
           const size_t e = e0 + b;
           float* po = a.part_o + e * 8 * kD + t;
 #pragma unroll
           for (int h = 0; h < kRows; ++h) {
             if (h < a.group) po[h * kD] = (__uint_as_float(o[h]) + __uint_as_float(o[8 + h])) * (1.0f / kPgScale);
-            if (lane == 0) {
-              a.part_l[(e * 4 + q) * 8 + h] = l[h];
-              if (q == 0) a.part_m[e * 8 + h] = seg_bad ? gone : -((h & 1) ? nM[h >> 1].y : nM[h >> 1].x);
-            }
+            if (lane == 0 && q == 0) a.part_m[e * 8 + h] = seg_bad ? gone : -((h & 1) ? nM[h >> 1].y : nM[h >> 1].x);
           }
+          if (lane % kPer == 0) a.part_l[(e * 4 + q) * 8 + lr] = l[0];
         }
       }
       x += nseg;
@@ -620,8 +648,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
     // The warpgroups' shares of one sequence meet at a common maximum. A NaN maximum (a missing
     // share) stays one.
     const int nw = w_end - w_cta;
-    const size_t e_first = static_cast<size_t>(hkv) * a.entries + w_cta +
-                           find_span(cs, a.pg.batch, pg_first_chunk(w_cta, chunks, workers));
+    const size_t e_first = static_cast<size_t>(hkv) * a.entries + w_cta + b_cta;
     const float* share = reinterpret_cast<const float*>(sm + kPgStageOff);
     const int pitch = NS * cbytes / 4;
     for (int i = tid; i < a.group * kD; i += kDecThreads) {
@@ -684,14 +711,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kvq_paged_merge(const MergeA
   if (plan.y < 0) return;                                    // refused
   // own shares: workers w0 .. of the first CTAs one by one, CTAs c_lo .. c_hi - 1 whose workers all
   // lie in the sequence by their first, the rest one by one
-  int w0 = 0, n_own = 0, n_lo = 0, n_mid = 0, per = 1, w_mid = 0;
+  const Shares sh(all.x, a.ctas);
+  const int per = sh.per_cta;
+  int w0 = 0, n_own = 0, n_lo = 0, n_mid = 0, w_mid = 0;
   if (plan.y > 0) {
-    w0 = pg_worker_of(plan.x, all.x, all.y);
-    const int w_end = pg_worker_of(plan.x + plan.y - 1, all.x, all.y) + 1;
-    per = pg_per_cta(all.y, a.ctas);
+    w0 = sh.of(plan.x);
+    const int w_end = sh.of(plan.x + plan.y - 1) + 1;
     int c_lo = w0 / per, c_hi = (w_end + per - 1) / per;
-    if (pg_first_chunk(c_lo * per, all.x, all.y) < plan.x) ++c_lo;
-    if (pg_first_chunk(min(c_hi * per, all.y), all.x, all.y) > plan.x + plan.y) --c_hi;
+    if (sh.first(c_lo * per) < plan.x) ++c_lo;
+    if (sh.first(min(c_hi * per, sh.workers)) > plan.x + plan.y) --c_hi;
     n_mid = max(0, c_hi - c_lo);
     if (n_mid > 0) {
       w_mid = c_lo * per;

@@ -80,7 +80,8 @@ struct KSlots {
 // wide one behind a narrow one. A whole warp, lane = slot.
 __device__ __forceinline__ bool k_slots(const uint32_t* slots, int n_cols, int stream_bits, KSlots& S) {
   const int s = threadIdx.x & 31, n = n_cols / 4;
-  const uint32_t e = s < n ? slots[s] : 0u;
+  const uint32_t in = s < kPlanSlots ? slots[s] : 0u;       // (loaded beside n_cols, not after it)
+  const uint32_t e = s < n ? in : 0u;
   uint32_t w = e & 15u, off = e >> 8;
   bool ok = w <= 8 && (w == 0 || off < static_cast<uint32_t>(stream_bits));
   if (!ok || w == 0) { w = 1; off = 0; }
@@ -137,9 +138,9 @@ __device__ __forceinline__ void k_wide_vals(uint32_t r0, uint32_t r1, uint32_t (
 
 // K-hat columns of slots first, first + step, .. below end (at most S.n) of the lane's token; kw: its
 // word 0 (word i at byte 128 i). put(slot, v) takes a slot's 4 columns. Narrow slots of every width go through one
-// sequence of instructions, two at a time. Words past the stream are read inside the stage and not
+// sequence of instructions, kAtOnce at a time. Words past the stream are read inside the stage and not
 // used.
-template <typename Put>
+template <int kAtOnce, typename Put>
 __device__ __forceinline__ void k_lookup(const uint8_t* kw, const KSlots& S, int first, int end, int step,
                                          uint32_t lane4, Put put) {
   end = min(end, S.n);
@@ -158,25 +159,36 @@ __device__ __forceinline__ void k_lookup(const uint8_t* kw, const KSlots& S, int
     put(s, v);
   }
 #pragma unroll 1
-  for (; s < end; s += 2 * step) {
-    const int k1 = s + step < end ? s + step : s;      // (an odd number of slots: the last is looked up twice)
-    const uint4 d[2] = {S.a[s], S.a[k1]};
-    const uint2 b[2] = {S.b[s], S.b[k1]};
-    uint32_t v[2][4];
+  for (; s < end; s += kAtOnce * step) {
+    // (past the last slot it is looked up again)
+    int at[kAtOnce];
+    uint4 d[kAtOnce];
+    uint32_t lb[kAtOnce], r0[kAtOnce], r1[kAtOnce];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kAtOnce; ++u) {
+      at[u] = (u == 0 || s + u * step < end) ? s + u * step : at[u - 1];
+      d[u] = S.a[at[u]];
+      const uint2 b = S.b[at[u]];
+      lb[u] = b.x | (lane4 & b.y);
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(kw + static_cast<int>(d[u].x));
       const uint32_t x0 = p[0], x1 = p[32], x2 = p[64];
-      const uint32_t r0 = __funnelshift_r(x0, x1, d[u].y), r1 = __funnelshift_r(x1, x2, d[u].y);
-      const uint32_t lb = b[u].x | (lane4 & b[u].y);
+      r0[u] = __funnelshift_r(x0, x1, d[u].y);
+      r1[u] = __funnelshift_r(x1, x2, d[u].y);
+    }
+    uint32_t v[kAtOnce][4];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t f = (k == 0) ? r0 : __funnelshift_r(r0, r1, d[u].z * k);
-        v[u][k] = lds32((f & d[u].w) | lb);
+        const uint32_t f = (k == 0) ? r0[u] : __funnelshift_r(r0[u], r1[u], d[u].z * k);
+        v[u][k] = lds32((f & d[u].w) | lb[u]);
       }
     }
-    put(s, v[0]);
-    put(k1, v[1]);
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) put(at[u], v[u]);
   }
 }
 

@@ -42,7 +42,7 @@ struct PrefixArgs {
   const kvq_head_alloc* alloc;
   PagedArgs pg;
   const int32_t* pages;                   // the prefix's pages
-  int len, splits, row_groups, n_stages;
+  int len, per, row_groups, n_stages;     // per: chunks of a split
   int low_p;                              // P' has low parts
   float* part_m;                          // [CTA][kPreRows]
   float* part_l;
@@ -171,9 +171,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
 
   const int n_tiles = (a.len + kTile - 1) / kTile;
   const int n_chunks_all = (n_tiles + kChunkTiles - 1) / kChunkTiles;
-  const int c_begin = static_cast<int>((static_cast<long long>(split) * n_chunks_all) / a.splits);
-  const int c_end = static_cast<int>((static_cast<long long>(split + 1) * n_chunks_all) / a.splits);
-  const int n = c_end - c_begin;                            // at least 1: splits never exceed the chunks
+  const int c_begin = split * a.per;
+  const int n = min(a.per, n_chunks_all - c_begin);         // at least 1: the host leaves no split empty
   const int rows = min(kPreRows, a.n_rows - rg * kPreRows);
 
   float M = -INFINITY, L = 0.0f;                            // row 32 q + lane, this warpgroup's tokens
@@ -331,7 +330,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
         if (!tc::mbar_wait(&S.fullk[s], rk.parity, WL)) *abort_flag = 1;
         rk.next(NS);
         const uint8_t* rec = stages + static_cast<size_t>(s) * cbytes + q * kbytes;
-        k_lookup(rec + lane4, S.slots, wg, kPlanSlots, 2, lane4, [&](int slot, const uint32_t (&v)[4]) {
+        k_lookup<4>(rec + lane4, S.slots, wg, kPlanSlots, 2, lane4, [&](int slot, const uint32_t (&v)[4]) {
           *reinterpret_cast<uint4*>(sm + kPreKOff + slot * 2048 + t * 16) = make_uint4(v[0], v[1], v[2], v[3]);
         });
         if (wg == (j & 1)) {
