@@ -460,9 +460,10 @@ def _code_of(dtype) -> int:
     if not _DTYPE_CODES:
         torch = _torch()
         _DTYPE_CODES.update({torch.float32: KVQ_F32, torch.float16: KVQ_F16, torch.bfloat16: KVQ_BF16})
-    if dtype not in _DTYPE_CODES:
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
         raise ValueError(f"unsupported dtype {dtype}")
-    return _DTYPE_CODES[dtype]
+    return code
 
 
 def _on_device(first, *rest) -> int:
@@ -483,13 +484,13 @@ def _stream_of(stream, dev: int) -> int:
 
 def _ints(t, name: str, rows, n) -> int:
     """Address of an int32 tensor [n] (rows -1) or [rows][n] with adjacent innermost elements; None: any size."""
+    got = t.shape
+    ok = len(got) == 1 if rows == -1 else len(got) == 2 and (rows is None or got[0] == rows)
+    if not ok or (n is not None and got[-1] != n):
+        raise ValueError(f"{name} has shape {tuple(got)}, expected {[n] if rows == -1 else [rows, n]}")
     if t.dtype is not _torch().int32:
         raise ValueError(f"{name} must be int32, not {t.dtype}")
-    got, st = t.shape, t.stride()
-    if len(got) != (1 if rows == -1 else 2) or (n is not None and got[-1] != n) or \
-            (rows is not None and rows >= 0 and got[0] != rows):
-        raise ValueError(f"{name} has shape {tuple(got)}, expected {[n] if rows == -1 else [rows, n]}")
-    if st[-1] != 1 and got[-1] > 1:
+    if t.stride()[-1] != 1 and got[-1] > 1:
         raise ValueError(f"{name} must have adjacent innermost elements")
     return t.data_ptr()
 
@@ -502,39 +503,42 @@ def _bytes(t, name: str, need: int) -> int:
 
 def _rows(t) -> Tensor4:
     """View of token rows [tokens][heads][128] as one sequence, or of [B][H][T][128] as it is."""
-    st = t.stride()
-    if t.shape[-1] > 1 and st[-1] != 1:
-        raise ValueError("last dimension must be contiguous")
-    if t.dim() == 3:
-        n, h, d = t.shape
-        return Tensor4(1, h, n, d, 0, st[1], st[0], _code_of(t.dtype), 0)
-    if t.dim() != 4:
+    sh, st = t.shape, t.stride()
+    if len(sh) not in (3, 4):
         raise ValueError("expected [tokens][heads][128] or [batch][heads][tokens][128]")
-    B, h, n, d = t.shape
-    return Tensor4(B, h, n, d, st[0], st[1], st[2], _code_of(t.dtype), 0)
+    if st[-1] != 1:
+        raise ValueError("last dimension must be contiguous")
+    if len(sh) == 3:
+        return Tensor4(1, sh[1], sh[0], sh[2], 0, st[1], st[0], _code_of(t.dtype), 0)
+    return Tensor4(sh[0], sh[1], sh[2], sh[3], st[0], st[1], st[2], _code_of(t.dtype), 0)
 
 
 def rope_desc(table, positions, axis=None) -> RopeDesc:
     """Rotation of block b by the angle of position positions[axis[b]][token]: table fp32
     [n_positions][64][2] of (cos, sin), positions int32 [n_axes][tokens] (or [tokens] for one axis), axis a
     sequence of 64 axis numbers (None: all 0). Keeps the tensors alive."""
-    if table.dtype != _torch().float32 or table.dim() != 3 or table.shape[1:] != (64, 2) or not table.is_contiguous():
+    sh = table.shape
+    if len(sh) != 3 or sh[1] != 64 or sh[2] != 2 or table.dtype is not _torch().float32 or not table.is_contiguous():
         raise ValueError("table must be contiguous fp32 [n_positions][64][2]")
     if positions.dim() == 1:
         positions = positions[None]
-    r = RopeDesc(table.data_ptr(), _ints(positions, "positions", None, None), positions.stride(0), table.shape[0],
-                 positions.shape[0])
+    at = _ints(positions, "positions", None, None)
+    n_axes, n_tokens = positions.shape
+    r = RopeDesc(table.data_ptr(), at, positions.stride(0), sh[0], n_axes)
     if axis is not None:
         if len(axis) != 64:
             raise ValueError("axis needs 64 entries")
-        ctypes.memmove(ctypes.addressof(r) + RopeDesc.axis.offset, bytes(axis), 64)
-    r.tensors = (table, positions)
+        ctypes.memmove(ctypes.addressof(r) + _AXIS_AT, bytes(axis), 64)
+    r.tensors, r.n_tokens = (table, positions), n_tokens
     return r
 
 
+_AXIS_AT = RopeDesc.axis.offset
+
+
 def _rope_tokens(rope, n: int) -> None:
-    if rope.tensors[1].shape[1] < n:
-        raise ValueError(f"{rope.tensors[1].shape[1]} positions for {n} tokens")
+    if rope.n_tokens < n:
+        raise ValueError(f"{rope.n_tokens} positions for {n} tokens")
 
 
 def kvq_rope(x, rope: RopeDesc, out=None, stream=None):
