@@ -223,10 +223,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
       tc::fence_after_sync();
       if (lane == 0) {
         const uint32_t d = tb + kPreS + 128u * (j & 1);
-        for (int ks = 0; ks < k_steps; ++ks)
-          tc::mma_ts(d, tb + 8 * ks, tc::sdesc(bk + 4096 * ks, 2048, 128), id, ks > 0 ? 1u : 0u);
-        for (int ks = 0; ks < k_steps; ++ks)
-          tc::mma_ss(d, tc::sdesc(smb + pre_q_step(ks), 2048, 128), tc::sdesc(bk + 4096 * ks, 2048, 128), id, 1u);
+        for (int ks = 0; ks < k_steps; ++ks) {
+          const uint64_t b = tc::sdesc(bk + 4096 * ks, 2048, 128);
+          tc::mma_ts(d, tb + 8 * ks, b, id, ks > 0 ? 1u : 0u);
+          tc::mma_ss(d, tc::sdesc(smb + pre_q_step(ks), 2048, 128), b, id, 1u);
+        }
         tc::mma_commit(&S.sfull[j & 1]);
         tc::mbar_arrive(&S.sfull[j & 1]);                   // (passes on the producers' norms)
       }
@@ -274,20 +275,25 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
     // Row r: q * f_b * log2(e) / sqrt(d) * 2^-e, its largest |value| in [0.5, 1). The rows are
     // staged in fp32 and taken up by row: columns 24 wg .. 24 wg + 23 of row t.
     float* stg = reinterpret_cast<float*>(sm + kPreKOff);
-    for (int r = warp; r < kPreRows; r += 16) {
-      const int row = rg * kPreRows + r;
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (r < rows) {
+    {
+      float v[kPreRows / 16][4];                            // (all rows' loads are in flight together)
+#pragma unroll
+      for (int i = 0; i < kPreRows / 16; ++i) {
+        const int r = warp + 16 * i, row = rg * kPreRows + r;
         const int b = row / a.group;
         const int64_t qi = b * a.qsb + (static_cast<int64_t>(hkv) * a.group + (row - b * a.group)) * a.qsh + lane;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = load_f32(a.q, a.q_dtype, qi + 32 * i) * S.dequant[(lane + 32 * i) % kH];
+        for (int k = 0; k < 4; ++k) v[i][k] = r < rows ? load_f32(a.q, a.q_dtype, qi + 32 * k) : 0.0f;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) stg[r * kPreQPitch + lane + 32 * i] = v[i];
+      for (int i = 0; i < kPreRows / 16; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          stg[(warp + 16 * i) * kPreQPitch + lane + 32 * k] = v[i][k] * S.dequant[(lane + 32 * k) % kH];
     }
     named_sync(1, 512);
     float mx = 0.0f;
+#pragma unroll 8
     for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(stg[t * kPreQPitch + 32 * wg + i]));
     S.xch[0][wg][t] = mx;
     named_sync(1, 512);
@@ -382,32 +388,36 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
         const float4* kn = reinterpret_cast<const float4*>(S.norm[j & 3][0] + 64 * cw);
         const float4* vn = reinterpret_cast<const float4*>(S.norm[j & 3][1] + 64 * cw);
         const int left = a.len - (c_begin + j) * kChunkTokens - 64 * cw;   // tokens of the prefix from the first one on
-        // logits over 2^e: S times the keys' norms, -inf past the prefix
-        auto logits = [&](int c0, float (&x)[16]) {
-          uint32_t sr[16];
-          tc::tmem_ld<16>(tS + c0, sr);
+        // logits over 2^e of 32 tokens: S times the keys' norms, -inf past the prefix
+        auto logits = [&](int c0, float2 (&x)[16]) {
+          uint32_t s0[16], s1[16];
+          tc::tmem_ld<16>(tS + c0, s0);
+          tc::tmem_ld<16>(tS + c0 + 16, s1);
           tc::wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 f = kn[(c0 + i) >> 2];
-            const float2 u = mul2(make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), make_float2(f.x, f.y));
-            const float2 v = mul2(make_float2(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])), make_float2(f.z, f.w));
-            x[i] = u.x; x[i + 1] = u.y; x[i + 2] = v.x; x[i + 3] = v.y;
+          for (int i = 0; i < 16; i += 2) {
+            const float4 f = kn[(c0 >> 2) + (i >> 1)];
+            const uint32_t* r = i < 8 ? s0 + 2 * i : s1 + 2 * i - 16;
+            x[i] = mul2(make_float2(__uint_as_float(r[0]), __uint_as_float(r[1])), make_float2(f.x, f.y));
+            x[i + 1] = mul2(make_float2(__uint_as_float(r[2]), __uint_as_float(r[3])), make_float2(f.z, f.w));
           }
           if (left < 64) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = c0 + i < left ? x[i] : -INFINITY;
+            for (int i = 0; i < 16; ++i) {
+              x[i].x = c0 + 2 * i < left ? x[i].x : -INFINITY;
+              x[i].y = c0 + 2 * i + 1 < left ? x[i].y : -INFINITY;
+            }
           }
         };
         float top = -INFINITY;
         if (live) {
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c0 = 0; c0 < 64; c0 += 16) {
-            float x[16];
+          for (int c0 = 0; c0 < 64; c0 += 32) {
+            float2 x[16];
             logits(c0, x);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
+            for (int i = 0; i < 16; ++i) m4[i & 3] = fmaxf(m4[i & 3], fmaxf(x[i].x, x[i].y));
           }
           top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qs;
         }
@@ -430,17 +440,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
               tc::fence_after_sync();
               const float2 al2 = make_float2(alpha, alpha);
 #pragma unroll
-              for (int c0 = 0; c0 < 64; c0 += 16) {
-                uint32_t o[16];
-                tc::tmem_ld<16>(tO + c0, o);
+              for (int c0 = 0; c0 < 64; c0 += 32) {
+                uint32_t o[2][16];
+                tc::tmem_ld<16>(tO + c0, o[0]);
+                tc::tmem_ld<16>(tO + c0 + 16, o[1]);
                 tc::wait_ld();
 #pragma unroll
-                for (int c = 0; c < 16; c += 2) {
-                  const float2 y = mul2(make_float2(__uint_as_float(o[c]), __uint_as_float(o[c + 1])), al2);
-                  o[c] = __float_as_uint(y.x);
-                  o[c + 1] = __float_as_uint(y.y);
+                for (int c = 0; c < 32; c += 2) {
+                  uint32_t* y = &o[c >> 4][c & 15];
+                  const float2 z = mul2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), al2);
+                  y[0] = __float_as_uint(z.x);
+                  y[1] = __float_as_uint(z.y);
                 }
-                tc::tmem_st<16>(tO + c0, o);
+                tc::tmem_st<16>(tO + c0, o[0]);
+                tc::tmem_st<16>(tO + c0 + 16, o[1]);
               }
             }
           }
@@ -449,35 +462,29 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
           float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int g0 = 0; g0 < 64; g0 += 32) {
-            float x[2][16];
-            logits(g0, x[0]);
-            logits(g0 + 16, x[1]);
+            float2 x[16];
+            logits(g0, x);
             uint32_t hi[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 f = vn[(g0 + i) >> 2];
+            for (int i = 0; i < 16; i += 2) {
+              const float4 f = vn[(g0 >> 2) + (i >> 1)];
 #pragma unroll
-              for (int k = i; k < i + 4; k += 2) {
-                float* xx = &x[k >> 4][k & 15];
-                const float2 z = fma2(make_float2(xx[0], xx[1]), qs2, nM);
+              for (int k = i; k < i + 2; ++k) {
+                const float2 z = fma2(x[k], qs2, nM);
                 const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
                 sum = add2(sum, p);
-                const float2 y = mul2(p, k == i ? make_float2(f.x, f.y) : make_float2(f.z, f.w));
-                const __half2 yh = __floats2half2_rn(y.x, y.y);
-                hi[k >> 1] = *reinterpret_cast<const uint32_t*>(&yh);
-                xx[0] = y.x;
-                xx[1] = y.y;
+                x[k] = mul2(p, k == i ? make_float2(f.x, f.y) : make_float2(f.z, f.w));
+                const __half2 yh = __floats2half2_rn(x[k].x, x[k].y);
+                hi[k] = *reinterpret_cast<const uint32_t*>(&yh);
               }
             }
             tc::tmem_st<16>(tS + g0, hi);
             if (a.low_p) {
 #pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                const float* xx = &x[k >> 4][k & 15];
-                const float2 r = fma2(__half22float2(*reinterpret_cast<const __half2*>(&hi[k >> 1])), make_float2(-1.0f, -1.0f),
-                                      make_float2(xx[0], xx[1]));
+              for (int k = 0; k < 16; ++k) {
+                const float2 r = fma2(__half22float2(*reinterpret_cast<const __half2*>(&hi[k])), make_float2(-1.0f, -1.0f), x[k]);
                 const __half2 yl = __floats2half2_rn(r.x, r.y);
-                hi[k >> 1] = *reinterpret_cast<const uint32_t*>(&yl);
+                hi[k] = *reinterpret_cast<const uint32_t*>(&yl);
               }
               tc::tmem_st<16>(tS + g0 + 16, hi);
             }
