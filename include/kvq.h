@@ -476,7 +476,8 @@ kvq_status kvq_paged_init(const void* alloc, const kvq_paged_desc* desc, void* p
  * tile is stored as code 0, norm 0; no other byte is touched. Rows from cu_tokens[batch] on
  * are not read. A sequence may get no token.
  * K, V: [1][n_kv_heads][n_tokens][128] (one dtype; strides may differ).
- * The pages written must belong to one sequence each. cu_tokens: [batch + 1], device memory.
+ * The pages written must belong to one sequence each; calls on one pool may overlap on the GPU if
+ * no page is written by one and used by another. cu_tokens: [batch + 1], device memory.
  * The call checks the pool's header on the device (KVQ_ERR_MISMATCH, nothing written) and every page
  * index, length and position it uses: a sequence whose rows or positions do not fit (rows not ascending
  * or past n_tokens, more positions than max_pages hold, a page outside the pool) loses the tiles
@@ -506,7 +507,7 @@ size_t kvq_paged_decode_workspace_bytes(const kvq_paged_desc* desc, int batch, i
  * sequence. A sequence with nothing to attend to gives a row of zeros.
  * q: [batch][n_q_heads][1][128], rotated (kvq_rope); n_q_heads / n_kv_heads must be 1..8.
  * out: [batch][n_q_heads][128], contiguous, 16-byte aligned, of out_dtype (any kvq_dtype,
- * rounded once from fp32).
+ * rounded once from fp32; for bf16 the prefix's softmax shares have 11 bits).
  * prefix: NULL or seq_len 0 for none.
  * ws: kvq_paged_decode_workspace_bytes bytes, zeroed once by kvq_workspace_init; calls that
  * share it must not overlap. Its status word reports (kvq_workspace_status) a header mismatch

@@ -951,6 +951,9 @@ bool rows_apart(const kvq_tensor4* t) {
   return true;
 }
 
+// Positions are 32-bit, with room for a chunk to be rounded up.
+constexpr long long kMaxPositions = 0x7fffffffLL - 4096;
+
 bool paged_ok(const kvq_paged_desc* d) {
   return d && d->n_pages >= 1 && d->page_tokens >= kTile && d->page_tokens % kTile == 0 && d->page_tokens <= 65536 &&
          d->n_kv_heads >= 1 && d->head_dim == kD && d->bits_k >= 1 && d->bits_k <= 8 && d->bits_v >= 1 && d->bits_v <= 8;
@@ -970,7 +973,7 @@ kvq_status paged_args(const kvq_paged_desc* d, const kvq_page_table* s, PagedArg
     if (!s->block_table || !s->seq_lens) return KVQ_ERR_ARG;
     if (s->batch < 1 || s->batch > kPagedMaxBatch || s->max_pages < 1) return KVQ_ERR_SHAPE;
     if (s->batch > 1 && s->table_stride < s->max_pages) return KVQ_ERR_ARG;
-    if (static_cast<long long>(s->max_pages) * d->page_tokens > 0x7fffffffLL) return KVQ_ERR_RANGE;   // positions are 32-bit
+    if (static_cast<long long>(s->max_pages) * d->page_tokens > kMaxPositions) return KVQ_ERR_RANGE;
     a.block_table = s->block_table;
     a.seq_lens = s->seq_lens;
     a.table_stride = s->table_stride;
@@ -1229,7 +1232,7 @@ kvq_status kvq_paged_decode_attn(const void* q, const kvq_tensor4* qd, const voi
   if (qd->seq_len != 1 || qd->batch != seqs->batch) return KVQ_ERR_SHAPE;
   if (qd->n_heads % d->n_kv_heads != 0 || qd->n_heads / d->n_kv_heads > 8) return KVQ_ERR_UNSUPPORTED;
   const int plen = prefix ? prefix->seq_len : 0;
-  if (plen < 0) return KVQ_ERR_RANGE;
+  if (plen < 0 || plen > kMaxPositions) return KVQ_ERR_RANGE;
   if (plen > 0) {
     if (!prefix->pages) return KVQ_ERR_ARG;
     if (plen > static_cast<long long>(prefix->n_pages) * d->page_tokens) return KVQ_ERR_RANGE;

@@ -227,8 +227,10 @@ __device__ __forceinline__ bool append_few(const uint8_t* krow, const uint8_t* v
     old0 = *reinterpret_cast<const uint2*>(vout + wk * kD + 2 * lane);
     old1 = *reinterpret_cast<const uint2*>(vout + wk * kD + kH + 2 * lane);
   }
-  const int w0 = al->width[2 * lane], w1 = al->width[2 * lane + 1];
   const int f0 = al->bit_off[2 * lane], f1 = al->bit_off[2 * lane + 1];
+  // (a block that would not end inside the key stream is left out: the words are the warp's own memory)
+  auto width = [&](int w, int f) { return w <= 8 && f >= 0 && f + 2 * w <= bits_k * kD ? w : 0; };
+  const int w0 = width(al->width[2 * lane], f0), w1 = width(al->width[2 * lane + 1], f1);
   const float2 g = *reinterpret_cast<const float2*>(al->gain + 2 * lane);
   float2 kl[kFewRows], kh[kFewRows], vl[kFewRows], vh[kFewRows];
 #pragma unroll

@@ -117,7 +117,7 @@ __device__ __forceinline__ int pg_scan(const PagedAttn& a, PgHeader& S, int* cs,
   if (n <= 32) {                          // a warp's scan, which every warp makes for itself
     const int lane = threadIdx.x & 31;
     const bool ok = len >= 0 && len <= room;
-    const int c = ok ? (len + kChunkTokens - 1) / kChunkTokens : 0;
+    const int c = ok ? len / kChunkTokens + (len % kChunkTokens != 0) : 0;
     int inc = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -144,7 +144,7 @@ __device__ __forceinline__ int pg_scan(const PagedAttn& a, PgHeader& S, int* cs,
     if (b < n) {
       if (b0 > 0) len = __ldg(a.pg.seq_lens + b);
       ok = len >= 0 && len <= room;
-      if (ok) c = (len + kChunkTokens - 1) / kChunkTokens;
+      if (ok) c = len / kChunkTokens + (len % kChunkTokens != 0);
       else record_status(a.status, KVQ_ERR_RANGE);
     }
     int total;

@@ -6,6 +6,7 @@ library's CUDA kernels. If libkvq.so is missing, the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -482,6 +483,12 @@ def _stream_of(stream, dev: int) -> int:
     return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _made_on(stream):
+    """Context in which a call on `stream` makes the buffers it was not given: their memory then belongs to that
+    stream, and a workspace is zeroed in its order."""
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
 def _ints(t, name: str, rows, n) -> int:
     """Address of an int32 tensor [n] (rows -1) or [rows][n] with adjacent innermost elements; None: any size."""
     got = t.shape
@@ -548,7 +555,8 @@ def kvq_rope(x, rope: RopeDesc, out=None, stream=None):
     dev = _on_device(x, out, *rope.tensors)
     xd = _rows(x)
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        with _made_on(stream):
+            out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif out.shape != x.shape:
         raise ValueError("out must have x's shape")
     od = xd if out is x else _rows(out)
@@ -581,7 +589,8 @@ def kvq_paged_decode_workspace(desc: PagedDesc, batch: int, n_q_heads: int, pref
 def kvq_paged_init(alloc, desc: PagedDesc, pool=None, stream=None):
     """Writes the header of a pool (uint8 device tensor, made if None); its pages stay as they are."""
     if pool is None:
-        pool = _empty_bytes(kvq_paged_bytes(desc), alloc.device)
+        with _made_on(stream):
+            pool = _empty_bytes(kvq_paged_bytes(desc), alloc.device)
     dev = _on_device(alloc, pool)
     _check("kvq_paged_init", lib().kvq_paged_init(_bytes(alloc, "alloc", kvq_alloc_bytes(desc.n_kv_heads)),
                                                   ctypes.byref(desc), _bytes(pool, "pool", kvq_paged_bytes(desc)),
@@ -620,12 +629,14 @@ def kvq_paged_decode_attn(q, pool, alloc, desc: PagedDesc, block_table, seq_lens
     B, Hq, d = q.shape
     dev = _on_device(q, pool, alloc, block_table, seq_lens, prefix_pages, out, ws)
     if out is None:
-        out = torch.empty_like(q, dtype=torch.float32 if out_dtype is None else out_dtype,
-                               memory_format=torch.contiguous_format)
+        with _made_on(stream):
+            out = torch.empty_like(q, dtype=torch.float32 if out_dtype is None else out_dtype,
+                                   memory_format=torch.contiguous_format)
     elif out.shape != q.shape or not out.is_contiguous() or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be contiguous, of q's shape and of out_dtype")
     if ws is None:
-        ws = kvq_paged_decode_workspace(desc, B, Hq, prefix_len, q.device)
+        with _made_on(stream):
+            ws = kvq_paged_decode_workspace(desc, B, Hq, prefix_len, q.device)
     qs = q.stride()
     if qs[2] != 1:
         raise ValueError("last dimension must be contiguous")

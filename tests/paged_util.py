@@ -96,7 +96,7 @@ class Paged:
         return kvq.kvq_paged_decode_attn(q, self.pool, self.alloc, self.desc, self.table, self.ints(lens),
                                          prefix_pages=self.prefix_pages if prefix else None, prefix_len=prefix, **kw)
 
-    def attention(self, q, lens, prefix=0):
+    def attention(self, q, lens, prefix=0, out=None):
         """(rows in 64 bits, bound of an fp32 kernel's error) for q [B][Hq][128].
 
         The bound counts the kernel's roundings at their worst. A logit is q' . k over at most 24
@@ -104,7 +104,10 @@ class Paged:
         the split of q' 2^-22 more): A 2^-17 in log2 units. p is off by that times ln 2, in the
         numerator and in the sum; sums over up to 2^12 tokens in at most 2^8 + 2^8 steps of 2^-22, and
         the exponential, the splits of p and the merges, are together below 2^-12. A weighted mean
-        of the values then moves by at most that share of the largest value."""
+        of the values then moves by at most that share of the largest value. For bf16 outputs (`out`) a prefix's
+        shares are rounded to fp16, 2^-11 more."""
+        import torch
+        shares = 2.0 ** -12 + (2.0 ** -11 if prefix and out == torch.bfloat16 else 0.0)
         q = host_f32(q).astype(np.float64)
         B, Hq, _ = q.shape
         G = Hq // self.hkv
@@ -121,7 +124,7 @@ class Paged:
                 p = np.exp(z - z.max())
                 out[b, h] = (p @ vv) / p.sum()
                 A = (np.abs(kk) @ np.abs(q[b, h])).max() / math.sqrt(128.0) * LOG2E
-                bound[b, h] = (2 * math.log(2) * A * 2.0 ** -17 + 2.0 ** -12) * np.abs(vv).max()
+                bound[b, h] = (2 * math.log(2) * A * 2.0 ** -17 + shares) * np.abs(vv).max()
         return out, bound
 
 

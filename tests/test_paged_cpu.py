@@ -159,6 +159,7 @@ def test_decode_refusals(L):
     assert call(seqs=_pages(mem, batch=0)) == SHAPE
     assert call(prefix=kvq.Prefix(mem, 2, -1)) == RANGE
     assert call(prefix=kvq.Prefix(mem, 2, 129)) == RANGE                            # longer than its pages
+    assert call(prefix=kvq.Prefix(mem, 1 << 30, 2 ** 31 - 1)) == RANGE              # no room to round up
     assert call(prefix=kvq.Prefix(None, 2, 100)) == ARG
     assert call(w=None) == WORKSPACE and call(wsb=1 << 10) == WORKSPACE
     need = kvq.kvq_paged_decode_workspace_bytes(D, 2, 16, 100)

@@ -290,7 +290,7 @@ def test_decode_splits(dev, batch, hkv, longest):
 @pytest.mark.parametrize("batch,hq,hkv,prefix,bits_k,bits_v,page,ot", [
     (1, 1, 1, 1, 3, 3, 32, "f32"), (4, 8, 1, 31, 4, 4, 64, "f32"), (5, 14, 2, 127, 2, 5, 32, "f16"), (8, 16, 2, 128, 3, 3, 128, "f32"),
     (9, 8, 1, 129, 8, 8, 64, "bf16"), (13, 7, 1, 300, 1, 1, 64, "f32"), (16, 8, 1, 1000, 3, 2, 64, "f32"), (33, 8, 1, 777, 2, 7, 32, "f32"),
-    (3, 24, 8, 2500, 4, 6, 256, "f32"), (2, 2, 2, 5000, 5, 3, 64, "f32")])
+    (3, 24, 8, 2500, 4, 6, 256, "f32"), (2, 2, 2, 5000, 5, 3, 64, "f32"), (17, 8, 1, 600, 3, 3, 64, "bf16"), (24, 12, 2, 1300, 2, 4, 128, "bf16")])
 def test_decode_behind_a_shared_prefix(dev, batch, hq, hkv, prefix, bits_k, bits_v, page, ot):
     import torch
     lens = ([0, 1, 40, 129, 64] * 7)[:batch]
@@ -300,7 +300,7 @@ def test_decode_behind_a_shared_prefix(dev, batch, hq, hkv, prefix, bits_k, bits
     ws = kvq.kvq_paged_decode_workspace(P.desc, batch, hq, prefix)
     got = P.decode(q, lens, prefix, out_dtype=_dt(ot), ws=ws)
     assert kvq.kvq_workspace_status(ws) == 0
-    check_rows(got, *P.attention(q, lens, prefix), _dt(ot))
+    check_rows(got, *P.attention(q, lens, prefix, _dt(ot)), _dt(ot))
     assert torch.equal(got, P.decode(q, lens, prefix, out_dtype=_dt(ot), ws=ws))
 
 
@@ -338,6 +338,107 @@ def test_a_nan_query_row_stays_in_its_row(dev):
         bad = torch.zeros((4, 8), dtype=torch.bool, device=dev)
         bad[1, 3] = bad[2, 0] = True
         assert bool(got[bad].isnan().all()) and torch.equal(got[~bad], want[~bad])
+
+
+def test_more_kv_heads_than_sms(dev):
+    """One CTA per head and more than one wave of them, own pages and prefix."""
+    import torch
+    lens = [40, 0, 130]
+    P = Paged(dev, 12, 160, 1, 1, 32, lens, prefix=70, profile_tokens=40)
+    P.fill(lens, torch.bfloat16, prefix=70)
+    q = torch.randn((3, 160, 128), device=dev)
+    for prefix in (0, 70):
+        check_rows(P.decode(q, lens, prefix), *P.attention(q, lens, prefix), torch.float32)
+
+
+def test_one_heads_allocation_swapped(dev):
+    """A call whose allocation differs for one KV head reports it and leaves that head's rows; the others are right."""
+    import torch
+    lens = [300, 90]
+    P = Paged(dev, 14, 2, 3, 3, 64, lens, prefix=200)
+    P.fill(lens, torch.bfloat16, prefix=200)
+    other = Paged(dev, 15, 2, 3, 3, 64, lens).alloc
+    alloc = P.alloc.clone()
+    alloc[2048:] = other[2048:]
+    q = torch.randn((2, 8, 128), device=dev)
+    for prefix in (0, 200):
+        ws = kvq.kvq_paged_decode_workspace(P.desc, 2, 8, prefix)
+        out = torch.full((2, 8, 128), 7.0, device=dev)
+        kvq.kvq_paged_decode_attn(q, P.pool, alloc, P.desc, P.table, P.ints(lens), prefix_pages=P.prefix_pages, prefix_len=prefix,
+                                  ws=ws, out=out)
+        assert kvq.kvq_workspace_status(ws) == kvq.KVQ_ERR_MISMATCH and bool((out[:, 4:] == 7.0).all())
+        want, bound = P.attention(q, lens, prefix)
+        check_rows(out[:, :4], want[:, :4], bound[:, :4], torch.float32)
+
+
+def test_calls_on_a_given_stream_without_buffers(dev):
+    """Outputs and workspaces that a call makes belong to the stream it was given."""
+    import torch
+    lens = [200, 33]
+    P = Paged(dev, 16, 2, 3, 3, 64, lens, prefix=150)
+    P.fill(lens, torch.bfloat16, prefix=150)
+    q = torch.randn((2, 8, 128), device=dev)
+    r = _desc(dev, angle_table(16), np.arange(2)[None], _axis(1))
+    want = [P.decode(q, lens, p) for p in (0, 150)] + [kvq.kvq_rope(q, r)]
+    ln = P.ints(lens)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(20):
+        torch.empty(1 << 24, dtype=torch.uint8, device=dev).fill_(255)          # memory that the next call may be given
+        got = [kvq.kvq_paged_decode_attn(q, P.pool, P.alloc, P.desc, P.table, ln, prefix_pages=P.prefix_pages, prefix_len=p, stream=side)
+               for p in (0, 150)] + [kvq.kvq_rope(q, r, stream=side)]
+    side.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
+
+
+def test_calls_that_overlap_on_two_streams(dev):
+    """Two batches over one pool, decoded and extended at once with a workspace each."""
+    import torch
+    lens = [260, 31, 500, 64]
+    P = Paged(dev, 17, 1, 4, 4, 64, [n + 40 for n in lens])
+    P.fill(lens, torch.bfloat16)
+    q = torch.randn((4, 8, 128), device=dev)
+    K, V = P.rows(40, torch.bfloat16)
+    halves = [slice(0, 2), slice(2, 4)]
+    streams = [torch.cuda.Stream() for _ in halves]
+    tabs, ws = [P.table[h].contiguous() for h in halves], [kvq.kvq_paged_decode_workspace(P.desc, 2, 8) for _ in halves]
+    l0, l1, cu = [P.ints(lens[h]) for h in halves], [P.ints([n + 10 for n in lens[h]]) for h in halves], P.ints([0, 10, 20])
+    qs, outs = [q[h].contiguous() for h in halves], [torch.empty((2, 8, 128), device=dev) for _ in halves]
+    torch.cuda.synchronize()
+    for i, s in enumerate(streams):
+        kvq.kvq_paged_append(K[20 * i:20 * i + 20], V[20 * i:20 * i + 20], P.alloc, P.desc, tabs[i], l0[i], cu, P.pool, stream=s)
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            kvq.kvq_paged_decode_attn(qs[i], P.pool, P.alloc, P.desc, tabs[i], l1[i], out=outs[i], ws=ws[i], stream=s)
+    torch.cuda.synchronize()
+    assert kvq.kvq_packed_status(P.pool) == 0 and all(kvq.kvq_workspace_status(w) == 0 for w in ws)
+    n = [x + 10 for x in lens]
+    check_rows(torch.cat(outs), *P.attention(q, n), torch.float32)
+
+
+@pytest.mark.parametrize("dtype,bits_k,bits_v", [("bf16", 4, 4), ("f16", 3, 7), ("f32", 2, 5), ("bf16", 8, 1), ("f16", 1, 8)])
+def test_tokens_one_by_one_equal_tiles_at_once(dev, dtype, bits_k, bits_v):
+    """One to four tokens a call (rows) and five or more (tiles) leave the same bytes, whatever the order of both."""
+    import torch
+    P = Paged(dev, 18, 2, bits_k, bits_v, 64, [130, 130, 130])
+    K, V = P.rows(130, _dt(dtype))
+    K[17] = 0.0                                                                  # a zero row: norm 0, codes at y = 0
+    V[18] = 0.0
+    K[19] *= 1e-6
+    pos = np.arange(130)[None] * 3
+    table = angle_table(400)
+    for b, steps in enumerate(([130], [1] * 130, [4, 1, 5, 2, 30, 3, 1, 33, 4, 31, 16])):
+        done = 0
+        for n in steps:
+            sl = slice(done, done + n)
+            P.append(K[sl], V[sl], [done], [0, n], table=P.table[b:b + 1].contiguous(), rope=_desc(dev, table, pos[:, sl], _axis(1)))
+            done += n
+        assert done == 130
+    got = [P.records(P.table_np[b])[:, :, :5] for b in range(3)]
+    np.testing.assert_array_equal(got[0], got[1])
+    np.testing.assert_array_equal(got[0], got[2])
 
 
 def test_decode_errors_leave_their_rows(dev):
