@@ -229,9 +229,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
   } else if (tid >= 192 && tid < 192 + kH) {
     S.dequant[tid - 192] = al->dequant[tid - 192] * (inv_sqrt_d * kLog2e);
   } else if (tid == 256) {
+    // (asked for before the header's fields are looked at, so one round trip brings everything)
+    const uint64_t dg = paged_digest(a.pool, hkv), ad = __ldcg(reinterpret_cast<const unsigned long long*>(&al->digest));
+    const int abk = __ldcg(&al->bits_k), akw = __ldcg(&al->k_words), apk = __ldcg(&al->plan_k_cols), aps = __ldcg(&al->plan_n_slots);
     unsigned code = paged_header_code(a.pool, a.pg);
-    const uint64_t dg = paged_digest(a.pool, hkv), ad = al->digest;
-    const int abk = al->bits_k, akw = al->k_words, apk = al->plan_k_cols, aps = al->plan_n_slots;
     if (!code && !((dg == ad) & (abk == a.pg.bits_k) & (akw == a.pg.bits_k * kD) & (apk <= 96) & (apk >= 8) & (aps >= 1) &
                    (aps <= kPlanSlots)))
       code = KVQ_ERR_MISMATCH;
@@ -412,12 +413,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
         if (h < a.group) {
           const int64_t qi = b * a.qsb + (static_cast<int64_t>(hkv) * a.group + h) * a.qsh + i4;
           const float4 f = *reinterpret_cast<const float4*>(S.dequant + i4);
-          const float ff[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i] = load_f32(a.q, a.q_dtype, qi + i) * ff[i];
-            v[4 + i] = load_f32(a.q, a.q_dtype, qi + kH + i) * ff[i];
-          }
+          by_dtype(a.q_dtype, [&](auto dt) {
+            const float4 lo = load4<dt.value>(a.q, qi), hi = load4<dt.value>(a.q, qi + kH);
+            v[0] = lo.x * f.x; v[1] = lo.y * f.y; v[2] = lo.z * f.z; v[3] = lo.w * f.w;
+            v[4] = hi.x * f.x; v[5] = hi.y * f.y; v[6] = hi.z * f.z; v[7] = hi.w * f.w;
+          });
         }
         float mx = 0.0f;
 #pragma unroll

@@ -10,8 +10,11 @@
 // widths 6..8 (the few blocks of the highest energy, or large budgets) take two single lookups.
 #pragma once
 
+#include <type_traits>
+
 #include "decode.cuh"
 #include "paged_pool.cuh"
+#include "quantize.cuh"
 
 namespace kvq {
 
@@ -205,6 +208,26 @@ __device__ __forceinline__ const uint8_t* paged_record(const uint8_t* pool, cons
     page = 0;
   }
   return pool + a.hdr_bytes + ((static_cast<size_t>(page) * a.n_kv_heads + hkv) * a.page_tiles + in) * a.rec_bytes;
+}
+
+// Elements i .. i + 3 of a row of 16-bit or fp32 values (i a multiple of 4, rows 16-byte aligned).
+template <int DT>
+__device__ __forceinline__ float4 load4(const void* p, int64_t i) {
+  if constexpr (DT == KVQ_F32) {
+    return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+    const float2 a = unpack_pair<DT>(u.x), b = unpack_pair<DT>(u.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+}
+// f(type) with the run-time dtype as a constant: loads inside one call of f are in flight together
+// (a branch on the type at every element makes each wait for the one before).
+template <typename F>
+__device__ __forceinline__ void by_dtype(int dtype, F f) {
+  if (dtype == KVQ_F32) f(std::integral_constant<int, KVQ_F32>{});
+  else if (dtype == KVQ_F16) f(std::integral_constant<int, KVQ_F16>{});
+  else f(std::integral_constant<int, KVQ_BF16>{});
 }
 
 // Element i of an output of run-time dtype.

@@ -151,9 +151,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
   } else if (tid >= 192 && tid < 192 + kH) {
     S.dequant[tid - 192] = al->dequant[tid - 192] * (inv_sqrt_d * kLog2e);
   } else if (tid == 256) {
+    // (asked for before the header's fields are looked at, so one round trip brings everything)
+    const uint64_t dg = paged_digest(a.pool, hkv), ad = __ldcg(reinterpret_cast<const unsigned long long*>(&al->digest));
+    const int abk = __ldcg(&al->bits_k), akw = __ldcg(&al->k_words), apk = __ldcg(&al->plan_k_cols), aps = __ldcg(&al->plan_n_slots);
     unsigned code = paged_header_code(a.pool, a.pg);
-    const uint64_t dg = paged_digest(a.pool, hkv), ad = al->digest;
-    const int abk = al->bits_k, akw = al->k_words, apk = al->plan_k_cols, aps = al->plan_n_slots;
     if (!code && !((dg == ad) & (abk == a.pg.bits_k) & (akw == a.pg.bits_k * kD) & (apk <= 96) & (apk >= 8) & (aps >= 1) &
                    (aps <= kPlanSlots)))
       code = KVQ_ERR_MISMATCH;
@@ -275,26 +276,36 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
     // Row r: q * f_b * log2(e) / sqrt(d) * 2^-e, its largest |value| in [0.5, 1). The rows are
     // staged in fp32 and taken up by row: columns 24 wg .. 24 wg + 23 of row t.
     float* stg = reinterpret_cast<float*>(sm + kPreKOff);
-    {
-      float v[kPreRows / 16][4];                            // (all rows' loads are in flight together)
+    by_dtype(a.q_dtype, [&](auto dt) {
+      float4 v[kPreRows / 16];                              // (all rows' loads are in flight together)
+      const float per = 1.0f / static_cast<float>(a.group);
 #pragma unroll
       for (int i = 0; i < kPreRows / 16; ++i) {
         const int r = warp + 16 * i, row = rg * kPreRows + r;
-        const int b = row / a.group;
-        const int64_t qi = b * a.qsb + (static_cast<int64_t>(hkv) * a.group + (row - b * a.group)) * a.qsh + lane;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[i][k] = r < rows ? load_f32(a.q, a.q_dtype, qi + 32 * k) : 0.0f;
+        const int b = static_cast<int>((static_cast<float>(row) + 0.5f) * per);   // row / group: rows are below 2^13
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows)
+          v[i] = load4<dt.value>(a.q, b * a.qsb + (static_cast<int64_t>(hkv) * a.group + (row - b * a.group)) * a.qsh + 4 * lane);
       }
+      const float4 f = *reinterpret_cast<const float4*>(S.dequant + (4 * lane) % kH);
 #pragma unroll
-      for (int i = 0; i < kPreRows / 16; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          stg[(warp + 16 * i) * kPreQPitch + lane + 32 * k] = v[i][k] * S.dequant[(lane + 32 * k) % kH];
-    }
+      for (int i = 0; i < kPreRows / 16; ++i) {
+        if (16 * i >= ((rows + 31) & ~31)) break;
+        float* x = stg + (warp + 16 * i) * kPreQPitch + 4 * lane;
+        x[0] = v[i].x * f.x;
+        x[1] = v[i].y * f.y;
+        x[2] = v[i].z * f.z;
+        x[3] = v[i].w * f.w;
+      }
+    });
     named_sync(1, 512);
+    // (rows past the batch come up to the warp's end as zeros; a warp of such rows alone takes no part: what its
+    // rows of Q', S and O hold concerns no other row)
     float mx = 0.0f;
+    if (live) {
 #pragma unroll 8
-    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(stg[t * kPreQPitch + 32 * wg + i]));
+      for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(stg[t * kPreQPitch + 32 * wg + i]));
+    }
     S.xch[0][wg][t] = mx;
     named_sync(1, 512);
     mx = fmaxf(fmaxf(S.xch[0][0][t], S.xch[0][1][t]), fmaxf(S.xch[0][2][t], S.xch[0][3][t]));
@@ -304,6 +315,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
     const float sc = ldexpf(1.0f, -e), qs = ldexpf(1.0f, e);
 #pragma unroll
     for (int c8 = 0; c8 < 24; c8 += 8) {
+      if (!live) break;
       uint32_t hi[8], lo[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
