@@ -503,7 +503,7 @@ def _ints(t, name: str, rows, n) -> int:
 
 
 def _bytes(t, name: str, need: int) -> int:
-    if t.element_size() != 1 or not t.is_contiguous() or t.numel() < need:
+    if t.itemsize != 1 or t.numel() < need or not t.is_contiguous():
         raise ValueError(f"{name} must be {need} contiguous bytes or more")
     return t.data_ptr()
 
@@ -574,6 +574,12 @@ def kvq_paged_bytes(desc: PagedDesc) -> int:
     return lib().kvq_paged_bytes(ctypes.byref(desc))
 
 
+def _pool_bytes(d: PagedDesc) -> int:
+    """kvq_paged_bytes of a valid descriptor (the library refuses another one) without a call."""
+    h = d.n_kv_heads
+    return (64 + 8 * h + 127) // 128 * 128 + d.n_pages * h * (d.page_tokens // TILE) * (512 * (d.bits_k + d.bits_v) + 128)
+
+
 def kvq_paged_decode_workspace_bytes(desc: PagedDesc, batch: int, n_q_heads: int, prefix_len: int = 0) -> int:
     return lib().kvq_paged_decode_workspace_bytes(ctypes.byref(desc), batch, n_q_heads, prefix_len)
 
@@ -615,8 +621,8 @@ def kvq_paged_append(K, V, alloc, desc: PagedDesc, block_table, seq_lens, cu_tok
         _rope_tokens(rope, kd.seq_len)
     _check("kvq_paged_append", lib().kvq_paged_append(
         K.data_ptr(), ctypes.byref(kd), V.data_ptr(), ctypes.byref(vd), ctypes.byref(rope) if rope is not None else None,
-        _bytes(alloc, "alloc", kvq_alloc_bytes(desc.n_kv_heads)), ctypes.byref(desc), ctypes.byref(seqs),
-        _ints(cu_tokens, "cu_tokens", -1, seqs.batch + 1), _bytes(pool, "pool", kvq_paged_bytes(desc)),
+        _bytes(alloc, "alloc", 2048 * desc.n_kv_heads), ctypes.byref(desc), ctypes.byref(seqs),
+        _ints(cu_tokens, "cu_tokens", -1, seqs.batch + 1), _bytes(pool, "pool", _pool_bytes(desc)),
         _stream_of(stream, dev)))
     return pool
 
@@ -648,8 +654,8 @@ def kvq_paged_decode_attn(q, pool, alloc, desc: PagedDesc, block_table, seq_lens
             raise ValueError("a prefix needs its pages")
         prefix = ctypes.byref(Prefix(_ints(prefix_pages, "prefix_pages", -1, None), prefix_pages.shape[0], prefix_len))
     _check("kvq_paged_decode_attn", lib().kvq_paged_decode_attn(
-        q.data_ptr(), ctypes.byref(qd), _bytes(pool, "pool", kvq_paged_bytes(desc)),
-        _bytes(alloc, "alloc", kvq_alloc_bytes(desc.n_kv_heads)), ctypes.byref(desc), ctypes.byref(seqs), prefix,
+        q.data_ptr(), ctypes.byref(qd), _bytes(pool, "pool", _pool_bytes(desc)),
+        _bytes(alloc, "alloc", 2048 * desc.n_kv_heads), ctypes.byref(desc), ctypes.byref(seqs), prefix,
         out.data_ptr(), _code_of(out.dtype), _bytes(ws, "ws", 0), ws.numel(), _stream_of(stream, dev)))
     return out
 

@@ -27,6 +27,7 @@ def test_sizes_follow_the_layout(L):
     for (n, page, h, bk, bv) in [(1, 32, 1, 1, 1), (10, 64, 2, 3, 3), (7, 256, 8, 4, 5), (3, 65536, 9, 8, 8)]:
         want = bg.header_bytes(h) + n * h * (page // 32) * bg.tile_record_bytes(128, bk, bv)
         assert kvq.kvq_paged_bytes(kvq.paged_desc(n, page, h, bk, bv)) == want
+        assert kvq._pool_bytes(kvq.paged_desc(n, page, h, bk, bv)) == want
     for bad in [(0, 64, 2, 3, 3), (4, 33, 2, 3, 3), (4, 0, 2, 3, 3), (4, 65568, 2, 3, 3), (4, 64, 0, 3, 3), (4, 64, 2, 0, 3),
                 (4, 64, 2, 9, 3), (4, 64, 2, 3, 0), (4, 64, 2, 3, 9), (4, 64, 2, 3, 3, 64)]:
         assert kvq.kvq_paged_bytes(kvq.paged_desc(*bad)) == 0, bad
