@@ -19,7 +19,7 @@
 namespace kvq {
 
 // Byte offsets of the tables, each a multiple of its size. The image sits at a shared-memory
-// address that is a multiple of 32 KB (plut_place), so that a field, the lane and a table's
+// address that is a multiple of 32 KB (kPlutAddr), so that a field, the lane and a table's
 // address have no bits in common.
 __host__ __device__ constexpr int plut_off(int w) {
   return w == 4 ? 0 : w == 3 ? 32768 : w == 2 ? 40960 : w == 1 ? 43008 : w == 8 ? 43520 : w == 7 ? 44032 : w == 6 ? 44288 : 45056;
