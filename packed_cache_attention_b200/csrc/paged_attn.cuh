@@ -356,8 +356,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
       if (!wait_warp(&S.kready[g], j & 1)) { ok = false; break; }
       tc::fence_after_sync();
       if (tc::elect_one()) {
-        for (int ks = 0; ks < k_steps; ++ks)
-          tc::mma_ts(tS, tbase + 8 * ks, tc::sdesc(bq + 512 * ks, 256, 128), id_s, ks > 0 ? 1u : 0u);
+        // (from the narrow blocks to the wide ones: sums are cut off at 24 bits after every step)
+        for (int ks = k_steps - 1; ks >= 0; --ks)
+          tc::mma_ts(tS, tbase + 8 * ks, tc::sdesc(bq + 512 * ks, 256, 128), id_s, ks < k_steps - 1 ? 1u : 0u);
         tc::mma_commit(&S.sfull[g]);
       }
       __syncwarp();
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
         }
         // ------------------------------------------------------------ P' (lane = token)
         {
-          const float2 vs2 = make_float2(vs, vs), minus1 = make_float2(-1.0f, -1.0f);
+          const float2 vs2 = make_float2(vs, vs), minus1 = make_float2(-1.0f, -1.0f), low_up = make_float2(kPgLow, kPgLow);
           uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
           for (int h = 0; h < kRows / 2; ++h) {
@@ -558,7 +559,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
             L[h] = add2(L[h], p);
             const float2 y = mul2(p, vs2);
             const __half2 yh = __floats2half2_rn(y.x, y.y);
-            const float2 r = fma2(__half22float2(yh), minus1, y);
+            const float2 r = mul2(fma2(__half22float2(yh), minus1, y), low_up);
             const __half2 yl = __floats2half2_rn(r.x, r.y);
             hi[h] = *reinterpret_cast<const uint32_t*>(&yh);
             lo[h] = *reinterpret_cast<const uint32_t*>(&yl);
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
           float* po = reinterpret_cast<float*>(my_stages) + t;
 #pragma unroll
           for (int h = 0; h < kRows; ++h) {
-            po[h * kD] = __uint_as_float(o[h]) + __uint_as_float(o[8 + h]);
+            po[h * kD] = __uint_as_float(o[h]) + __uint_as_float(o[8 + h]) * (1.0f / kPgLow);
             if (lane == 0 && q == 0) S.join_m[g][h] = seg_bad ? gone : -((h & 1) ? nM[h >> 1].y : nM[h >> 1].x);
           }
           if (lane % kPer == 0) S.join_l[g][q][lr] = l[0];
@@ -615,7 +616,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
           float* po = a.part_o + e * 8 * kD + t;
 #pragma unroll
           for (int h = 0; h < kRows; ++h) {
-            if (h < a.group) po[h * kD] = (__uint_as_float(o[h]) + __uint_as_float(o[8 + h])) * (1.0f / kPgScale);
+            if (h < a.group) po[h * kD] = (__uint_as_float(o[h]) + __uint_as_float(o[8 + h]) * (1.0f / kPgLow)) * (1.0f / kPgScale);
             if (lane == 0 && q == 0) a.part_m[e * 8 + h] = seg_bad ? gone : -((h & 1) ? nM[h >> 1].y : nM[h >> 1].x);
           }
           if (lane % kPer == 0) a.part_l[(e * 4 + q) * 8 + lr] = l[0];

@@ -237,10 +237,13 @@ __device__ __forceinline__ void store_f32(void* p, int dtype, int64_t i, float v
   else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
-// Running maxima move when a logit exceeds them by more than 2^6 (log2 units); P' is stored
-// times 2^-3, at most 2^3 * 65504 / sqrt(128), inside fp16, and its low parts end 2^-22 below the
-// largest share.
-constexpr int kPgThr = 6;
-constexpr float kPgScale = 0.125f;
+// Shares P' = 2^(logit - maximum) * |value| / sqrt(128) * scale as fp16 pairs. A running maximum moves
+// when a logit exceeds it by more than `thr` (log2 units), and 2^thr * 65504 / sqrt(128) * scale stays
+// inside fp16. Where low parts have rows of their own in the product (decode) they are stored times
+// 2^11, so that a share's pair is good to 2^-22 however small it is. Where they join the high parts' sums
+// (prefix) they end at fp16's 2^-25: the scale is the larger there, and the maxima move sooner, which a
+// chunk's time does not show (2.79 us; for decode the same costs 3 %).
+constexpr int kPgThr = 6, kPreThr = 2;
+constexpr float kPgScale = 0.125f, kPreScale = 2.0f, kPgLow = 2048.0f;
 
 }  // namespace kvq

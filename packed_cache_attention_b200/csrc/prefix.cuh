@@ -226,11 +226,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
       tc::fence_after_sync();
       if (tc::elect_one()) {
         const uint32_t d = tb + kPreS + 128u * (j & 1);
-        for (int ks = 0; ks < k_steps; ++ks) {
-          const uint64_t b = tc::sdesc(bk + 4096 * ks, 2048, 128);
-          tc::mma_ts(d, tb + 8 * ks, b, id, ks > 0 ? 1u : 0u);
-          tc::mma_ss(d, tc::sdesc(smb + pre_q_step(ks), 2048, 128), b, id, 1u);
-        }
+        // The products' sums are cut off at 24 bits after every step: the small terms first (low parts, and
+        // from the narrow blocks to the wide ones). High and low step by step from the wide end was up to
+        // twice as far from the exact output.
+        for (int ks = k_steps - 1; ks >= 0; --ks)
+          tc::mma_ss(d, tc::sdesc(smb + pre_q_step(ks), 2048, 128), tc::sdesc(bk + 4096 * ks, 2048, 128), id, ks < k_steps - 1 ? 1u : 0u);
+        for (int ks = k_steps - 1; ks >= 0; --ks) tc::mma_ts(d, tb + 8 * ks, tc::sdesc(bk + 4096 * ks, 2048, 128), id, 1u);
         tc::mma_commit(&S.sfull[j & 1]);
         tc::mbar_arrive(&S.sfull[j & 1]);                   // (passes on the producers' norms)
       }
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
           const bool valid = (c_begin + j) * kChunkTokens + t < a.len;
           const uint16_t* nrm = reinterpret_cast<const uint16_t*>(rec + 4 * kD * a.pg.bits_k) + lane;
           S.norm[j & 3][0][t] = valid ? __half2float(__ushort_as_half(nrm[0])) : 0.0f;
-          S.norm[j & 3][1][t] = valid ? __half2float(__ushort_as_half(nrm[kTile])) * (inv_sqrt_d * kPgScale) : 0.0f;
+          S.norm[j & 3][1][t] = valid ? __half2float(__ushort_as_half(nrm[kTile])) * (inv_sqrt_d * kPreScale) : 0.0f;
         }
         tc::fence_proxy_async_smem();
         tc::fence_before_sync();
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
         }
         if (live) {
           const float cm = fmaxf(S.xch[j & 1][0][t], S.xch[j & 1][1][t]);
-          const bool up = cm > M + static_cast<float>(kPgThr);
+          const bool up = cm > M + static_cast<float>(kPreThr);
           if (__any_sync(0xffffffffu, up)) {
             const float mn = up ? cm : M;
             const float alpha = (M == -INFINITY) ? 0.0f : fast_exp2(M - mn);
@@ -544,8 +545,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
         if (t < rows) {
 #pragma unroll
           for (int c = 0; c < 16; c += 4)
-            po[(c0 + c) >> 2] = make_float4(__uint_as_float(o[c]) * (1.0f / kPgScale), __uint_as_float(o[c + 1]) * (1.0f / kPgScale),
-                                            __uint_as_float(o[c + 2]) * (1.0f / kPgScale), __uint_as_float(o[c + 3]) * (1.0f / kPgScale));
+            po[(c0 + c) >> 2] = make_float4(__uint_as_float(o[c]) * (1.0f / kPreScale), __uint_as_float(o[c + 1]) * (1.0f / kPreScale),
+                                            __uint_as_float(o[c + 2]) * (1.0f / kPreScale), __uint_as_float(o[c + 3]) * (1.0f / kPreScale));
         }
       }
     }
