@@ -10,7 +10,7 @@
 // Precision: Q' and P' are fp16 high + low parts (Khat and Vhat are fp16 centroids, exact), so every
 // product runs twice; the norms of keys and values multiply the fp32 logits and shares. A
 // single fp16 Q' would move a logit of 100 by 2^-5. For bf16 outputs P' has its high part alone: a
-// share is then off by at most 2^-11 of itself, a quarter of the output's own rounding (2^-9).
+// share is then off by at most 2^-11 of itself, an eighth of the output's own rounding (2^-8).
 //
 // Layout. Tensor memory: Q' high (A operand, 96 columns), two buffers of 128 columns for S, O. A
 // warpgroup writes its P' over the S columns that it has read (16 columns high parts, 16 low).
@@ -19,9 +19,9 @@
 // of a token's key, or 8 tokens of a dim) are one 16-byte store next to its neighbour lane's.
 //
 // Order: the producers write Khat(j + 1) once S(j) is done and Vhat(j) once O(j - 1) is; S(j + 1) is
-// issued before O(j), into the other buffer, so it runs under the softmax of chunk j. With all
-// warps taking every step in turn a chunk took 5.9k cycles; with tokens as lanes, whose row maxima
-// need a warp reduction per row, 12.9k.
+// issued before O(j), into the other buffer, so it runs under the softmax of chunk j. A chunk takes
+// 5.3k cycles (K3V3, 128 rows); with tokens as lanes, whose row maxima need a warp reduction per
+// row, it took 12.9k.
 //
 // Every wait is bounded, as in kvq_decode_gtq; a CTA that gave up, or met a bad header or page,
 // leaves NaN maxima, at which the merge leaves the rows as they are.
