@@ -54,7 +54,8 @@ struct PrefixArgs {
 
 struct PreHeader {
   uint64_t fullk[kPgStagesMax], fullv[kPgStagesMax];
-  uint64_t kready, sfull[2], vready, ofull, drain, setup;   // sfull by chunk parity: see the consumers
+  uint64_t kready, ofull, drain, setup;
+  uint64_t sfull[2], vready[2];                 // by chunk parity: see the consumers
   uint32_t tmem_base;
   int bad, bad_page, abort;
   int k_cols;
@@ -119,7 +120,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
     tc::mbar_init(&S.kready, 8);
     tc::mbar_init(&S.sfull[0], 2);
     tc::mbar_init(&S.sfull[1], 2);
-    tc::mbar_init(&S.vready, 16);
+    tc::mbar_init(&S.vready[0], 16);
+    tc::mbar_init(&S.vready[1], 16);
     tc::mbar_init(&S.ofull, 1);
     tc::mbar_init(&S.drain, 2);
     tc::mbar_init(&S.setup, 1);
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
     bool ok = logits(0);
     for (int j = 0; j < n && ok; ++j) {
       if (j + 1 < n && !logits(j + 1)) { ok = false; break; }
-      if (!wait_warp(&S.vready, j & 1)) { ok = false; break; }
+      if (!wait_warp(&S.vready[j & 1], (j >> 1) & 1)) { ok = false; break; }
       tc::fence_after_sync();
       if (lane == 0) {
         const uint32_t p = tb + kPreS + 128u * (j & 1);
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&S.vready);
+        if (lane == 0) tc::mbar_arrive(&S.vready[j & 1]);
       }
     } else {
       // ---------------------------------------------------------------- consumers: softmax (lane = row)
@@ -397,7 +399,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
       bool stopped = false;
       for (int j = 0; j < n; ++j) {
         // S(j + 1) may be done before a warp that lags gets here, S(j + 2) not (it needs O(j)): two
-        // barriers tell their phases apart
+        // barriers tell their phases apart. For the same reason P'(j + 1) may be ready (its rows are few,
+        // or the warp has none) before the last producer has Vhat(j): on one barrier that arrival
+        // would stand in for the producer's, and O(j) would read a Vhat that is not there yet.
         if (!tc::mbar_wait(&S.sfull[j & 1], (j >> 1) & 1, WL)) *abort_flag = 1;
         tc::fence_after_sync();
         const uint32_t tS = tb + kPreS + 128u * (j & 1) + lane_base + 64 * cw;
@@ -510,7 +514,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&S.vready);
+        if (lane == 0) tc::mbar_arrive(&S.vready[j & 1]);
       }
       if (!stopped) {
         if (!tc::mbar_wait(&S.ofull, (n - 1) & 1, WL)) *abort_flag = 1;

@@ -304,6 +304,23 @@ def test_decode_behind_a_shared_prefix(dev, batch, hq, hkv, prefix, bits_k, bits
     assert torch.equal(got, P.decode(q, lens, prefix, out_dtype=_dt(ot), ws=ws))
 
 
+@pytest.mark.parametrize("batch,hq,hkv,bits_k,bits_v", [(1, 16, 16, 8, 8), (1, 32, 16, 1, 8), (5, 64, 8, 6, 8), (3, 64, 8, 8, 3)])
+def test_a_prefix_whose_values_are_ready_late(dev, batch, hq, hkv, bits_k, bits_v):
+    """Warps without query rows are done with a chunk's softmax at once, while its values (wide, one stage of
+    copies) are still looked up: the products wait for them, and every call gives the same bits."""
+    import torch
+    prefix, lens = 9000, [3] * batch                                                # 4 to 8 chunks a CTA
+    P = Paged(dev, 40 + bits_v, hkv, bits_k, bits_v, 256, lens, prefix=prefix)
+    P.fill(lens, torch.bfloat16, prefix=prefix)
+    q = torch.randn((batch, hq, 128), device=dev).to(torch.bfloat16)
+    ws = kvq.kvq_paged_decode_workspace(P.desc, batch, hq, prefix)
+    got = P.decode(q, lens, prefix, ws=ws)
+    check_rows(got, *P.attention(q, lens, prefix), torch.float32)
+    for _ in range(50):
+        assert torch.equal(got, P.decode(q, lens, prefix, ws=ws))
+    assert kvq.kvq_workspace_status(ws) == 0
+
+
 def test_a_logit_far_above_the_rest_and_rows_of_zeros(dev):
     """Keys that grow along the prefix move the running maximum in every chunk; one row's query is zero,
     one huge, one tiny."""
