@@ -507,7 +507,7 @@ size_t kvq_paged_decode_workspace_bytes(const kvq_paged_desc* desc, int batch, i
  * sequence. A sequence with nothing to attend to gives a row of zeros.
  * q: [batch][n_q_heads][1][128], rotated (kvq_rope); n_q_heads / n_kv_heads must be 1..8.
  * out: [batch][n_q_heads][128], contiguous, 16-byte aligned, of out_dtype (any kvq_dtype,
- * rounded once from fp32; for bf16 the prefix's softmax shares have 11 bits).
+ * rounded once from fp32: the rows of a 16-bit type are the fp32 ones rounded).
  * prefix: NULL or seq_len 0 for none.
  * ws: kvq_paged_decode_workspace_bytes bytes, zeroed once by kvq_workspace_init; calls that
  * share it must not overlap. Its status word reports (kvq_workspace_status) a header mismatch

@@ -1278,7 +1278,6 @@ kvq_status kvq_paged_decode_attn(const void* q, const kvq_tensor4* qd, const voi
     a.len = plen;
     a.per = per;
     a.row_groups = pp.groups;
-    a.low_p = out_dtype != KVQ_BF16;
     a.part_m = reinterpret_cast<float*>(w8 + w.pre_m);
     a.part_l = reinterpret_cast<float*>(w8 + w.pre_l);
     a.part_o = reinterpret_cast<float*>(w8 + w.pre_o);

@@ -9,8 +9,8 @@
 //
 // Precision: Q' and P' are fp16 high + low parts (Khat and Vhat are fp16 centroids, exact), so every
 // product runs twice; the norms of keys and values multiply the fp32 logits and shares. A
-// single fp16 Q' would move a logit of 100 by 2^-5. For bf16 outputs P' has its high part alone: a
-// share is then off by at most 2^-11 of itself, an eighth of the output's own rounding (2^-8).
+// single fp16 Q' would move a logit of 100 by 2^-5. The output's type makes no difference up to its
+// rounding.
 //
 // Layout. Tensor memory: Q' high (A operand, 96 columns), two buffers of 128 columns for S, O. A
 // warpgroup writes its P' over the S columns that it has read (16 columns high parts, 16 low).
@@ -43,7 +43,6 @@ struct PrefixArgs {
   PagedArgs pg;
   const int32_t* pages;                   // the prefix's pages
   int len, per, row_groups, n_stages;     // per: chunks of a split
-  int low_p;                              // P' has low parts
   float* part_m;                          // [CTA][kPreRows]
   float* part_l;
   float* part_o;                          // [CTA][kPreRows][128]
@@ -250,7 +249,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
         const uint32_t p = tb + kPreS + 128u * (j & 1);
 #pragma unroll
         for (int ks = 0; ks < 2 * (kChunkTokens / 16); ++ks) {
-          if (ks >= kChunkTokens / 16 && !a.low_p) break;
           const int kk = ks % (kChunkTokens / 16);          // high parts, then low parts
           tc::mma_ts(tb + kPreO, p + 32 * (kk >> 1) + 8 * (kk & 1) + (ks >= kChunkTokens / 16 ? 16 : 0),
                      tc::sdesc(bv + 4096 * kk, 2048, 128), id, (j > 0 || ks > 0) ? 1u : 0u);
@@ -499,15 +497,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
               }
             }
             tc::tmem_st<16>(tS + g0, hi);
-            if (a.low_p) {
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const float2 r = fma2(__half22float2(*reinterpret_cast<const __half2*>(&hi[k])), make_float2(-1.0f, -1.0f), x[k]);
-                const __half2 yl = __floats2half2_rn(r.x, r.y);
-                hi[k] = *reinterpret_cast<const uint32_t*>(&yl);
-              }
-              tc::tmem_st<16>(tS + g0 + 16, hi);
+            for (int k = 0; k < 16; ++k) {
+              const float2 r = fma2(__half22float2(*reinterpret_cast<const __half2*>(&hi[k])), make_float2(-1.0f, -1.0f), x[k]);
+              const __half2 yl = __floats2half2_rn(r.x, r.y);
+              hi[k] = *reinterpret_cast<const uint32_t*>(&yl);
             }
+            tc::tmem_st<16>(tS + g0 + 16, hi);
           }
           L += sum.x + sum.y;
         }

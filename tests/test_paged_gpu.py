@@ -321,6 +321,20 @@ def test_a_prefix_whose_values_are_ready_late(dev, batch, hq, hkv, bits_k, bits_
     assert kvq.kvq_workspace_status(ws) == 0
 
 
+@pytest.mark.parametrize("batch,hq,hkv,prefix,bits_k,bits_v", [(9, 8, 1, 129, 3, 3), (64, 16, 2, 3000, 3, 3), (5, 14, 2, 1000, 8, 8),
+                                                              (4, 4, 1, 0, 4, 4)])
+def test_16_bit_outputs_are_the_fp32_ones_rounded(dev, batch, hq, hkv, prefix, bits_k, bits_v):
+    """The output's type changes its rounding alone, not what is computed."""
+    import torch
+    lens = ([0, 1, 40, 129, 64, 300] * 11)[:batch]
+    P = Paged(dev, 50 + batch, hkv, bits_k, bits_v, 64, lens, prefix=prefix)
+    P.fill(lens, torch.bfloat16, prefix=prefix)
+    q = torch.randn((batch, hq, 128), device=dev).to(torch.bfloat16)
+    want = P.decode(q, lens, prefix)
+    for dt in (torch.bfloat16, torch.float16):
+        assert torch.equal(P.decode(q, lens, prefix, out_dtype=dt), want.to(dt))
+
+
 def test_a_logit_far_above_the_rest_and_rows_of_zeros(dev):
     """Keys that grow along the prefix move the running maximum in every chunk; one row's query is zero,
     one huge, one tiny."""
