@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
         tc::fence_proxy_async_smem();
         named_sync(1 + g, 128);
       }
-      float2 nM[kRows / 2], L[kRows / 2];                   // minus the running maxima; this lane's row sums
+      float2 nM[kRows / 2], L[kRows / 2];                   // minus the running maxima (-M); this lane's row sums
 #pragma unroll
       for (int h = 0; h < kRows / 2; ++h) {
         nM[h] = make_float2(INFINITY, INFINITY);
@@ -477,7 +477,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
         const bool valid = (c_first + i) * kChunkTokens + t < len;
         const uint16_t* nrm = reinterpret_cast<const uint16_t*>(sv + q * vbytes) + lane;
         const float kn = valid ? __half2float(__ushort_as_half(nrm[0])) : 0.0f;
-        const float vs = valid ? __half2float(__ushort_as_half(nrm[kTile])) * (inv_sqrt_d * kPgScale) : 0.0f;
+        const float vn = valid ? __half2float(__ushort_as_half(nrm[kTile])) * inv_sqrt_d : 0.0f;
+        const float vs = vn * kPgScale, lv = share_log2(vn);
         {
           uint32_t v16[16];
           const uint32_t* vw = reinterpret_cast<const uint32_t*>(sv + 4 * kTile) + t;
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
             tc::tmem_st<16>(tbase + kPgVCol + lane_base + 16 * u, v16);
           }
         }
-        // ------------------------------------------------------------ logits minus the maxima
+        // ------------------------------------------------------------ logits minus M (see kPgThr)
         float2 xv[kRows / 2], z[kRows / 2];
         {
           uint32_t sr[16];
@@ -511,14 +512,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
         bool over = false;
 #pragma unroll
         for (int h = 0; h < kRows / 2; ++h)
-          over |= (z[h].x > static_cast<float>(kPgThr)) | (z[h].y > static_cast<float>(kPgThr));
+          over |= (z[h].x > static_cast<float>(kPgThr) - lv) | (z[h].y > static_cast<float>(kPgThr) - lv);
         // a wait that gave up joins the vote, so that the four warps stop as one
         const bool stop = *abort_flag != 0;
         if (named_sync_or(1 + g, 128, over || stop)) {
           if (stop) S.wg_stop[g] = 1;
 #pragma unroll
           for (int h = 0; h < kRows; ++h) {
-            const int m = __reduce_max_sync(0xffffffffu, ordered((h & 1) ? xv[h >> 1].y : xv[h >> 1].x));
+            const int m = __reduce_max_sync(0xffffffffu, ordered(((h & 1) ? xv[h >> 1].y : xv[h >> 1].x) + lv));
             if (lane == 0) S.xch[g][q][h] = from_ordered(m);
           }
           named_sync(1 + g, 128);

@@ -237,13 +237,23 @@ __device__ __forceinline__ void store_f32(void* p, int dtype, int64_t i, float v
   else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
-// Shares P' = 2^(logit - maximum) * |value| / sqrt(128) * scale as fp16 pairs. A running maximum moves
-// when a logit exceeds it by more than `thr` (log2 units), and 2^thr * 65504 / sqrt(128) * scale stays
-// inside fp16. Where low parts have rows of their own in the product (decode) they are stored times
-// 2^11, so that a share's pair is good to 2^-22 however small it is. Where they join the high parts' sums
-// (prefix) they end at fp16's 2^-25: the scale is the larger there, and the maxima move sooner, which a
-// chunk's time does not show (2.79 us; for decode the same costs 3 %).
+// Shares P' = 2^(logit - M) * |value| / sqrt(128) * scale as fp16 pairs. M is a row's running maximum not
+// of its logits but of logit + log2(|value| / sqrt(128)): the largest share is in [scale, 2^thr scale]
+// whatever the values' norms are, and the row sum, with the same M, is fp32. M moves when it is
+// exceeded by more than `thr` (log2 units); 2^thr * scale = 2^15 stays inside fp16. A pair is good to
+// 2^-22 of its share down to fp16's smallest normal number in the high part, and below that to an
+// absolute error: 2^-36 where low parts have rows of their own in the product and are stored times
+// 2^11 (decode), 2^-25 where they join the high parts' sums (prefix); that is 2^-45 and 2^-38 of the
+// row's largest share. (M of the logits alone and a fixed scale lost the shares of small values:
+// outputs off by 7e-4 at |v| = 1e-3 and 0.1 at 1e-5. The maxima of the prefix move sooner, which a chunk's
+// time does not show; for decode the same costs 3 %.)
 constexpr int kPgThr = 6, kPreThr = 2;
-constexpr float kPgScale = 0.125f, kPreScale = 2.0f, kPgLow = 2048.0f;
+constexpr float kPgScale = 512.0f, kPreScale = 8192.0f, kPgLow = 2048.0f;
+
+// log2 of a value's norm / sqrt(128) for M. Stored norms are 0 or 2^-24 .. 65504. A value of norm 0 counts
+// as 2^-60: shares of other values stay exact when all of them together are 2^-60 of such a token's
+// softmax weight, and row sums stay below 2^97. An infinite or NaN norm (its share is not finite
+// anyway) counts as one inside the range.
+__device__ __forceinline__ float share_log2(float vn) { return fminf(fmaxf(__log2f(vn), -60.0f), 13.0f); }
 
 }  // namespace kvq

@@ -61,8 +61,8 @@ struct PreHeader {
   KSlots slots;
   alignas(16) float dequant[kH];
   int8_t col_block[96];
-  alignas(16) float norm[4][2][kChunkTokens];   // [chunk mod 4][key, value / sqrt(d)][token]
-  float xch[2][4][kPreRows];                    // [chunk parity][softmax warpgroup][row]: maximum; sums at the end
+  alignas(16) float norm[4][3][kChunkTokens];   // [chunk mod 4][key, value / sqrt(d), its log2 for M][token]
+  float xch[2][2][kPreRows];                    // [chunk parity][softmax warpgroup][row]: maximum; sums at the end
 };
 
 // Shared memory: header, Q' low of the first kPreQCut K steps; lookup tables (at their address); Q'
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
   const int n = min(a.per, n_chunks_all - c_begin);         // at least 1: the host leaves no split empty
   const int rows = min(kPreRows, a.n_rows - rg * kPreRows);
 
-  float M = -INFINITY, L = 0.0f;                            // row 32 q + lane, this warpgroup's tokens
+  float M = -INFINITY, L = 0.0f;                            // row 32 q + lane (see kPreThr); this warpgroup's tokens
 
   if (bad) {
   } else if (is_issuer) {
@@ -310,9 +310,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
 #pragma unroll 8
       for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(stg[t * kPreQPitch + 32 * wg + i]));
     }
-    S.xch[0][wg][t] = mx;
+    S.xch[wg >> 1][wg & 1][t] = mx;
     named_sync(1, 512);
-    mx = fmaxf(fmaxf(S.xch[0][0][t], S.xch[0][1][t]), fmaxf(S.xch[0][2][t], S.xch[0][3][t]));
+    mx = fmaxf(fmaxf(S.xch[0][0][t], S.xch[0][1][t]), fmaxf(S.xch[1][0][t], S.xch[1][1][t]));
     int e = 0;
     if (mx > 0.0f) frexpf(mx, &e);
     e = max(e, -126);                                       // 2^-e stays finite
@@ -359,7 +359,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
           const bool valid = (c_begin + j) * kChunkTokens + t < a.len;
           const uint16_t* nrm = reinterpret_cast<const uint16_t*>(rec + 4 * kD * a.pg.bits_k) + lane;
           S.norm[j & 3][0][t] = valid ? __half2float(__ushort_as_half(nrm[0])) : 0.0f;
-          S.norm[j & 3][1][t] = valid ? __half2float(__ushort_as_half(nrm[kTile])) * (inv_sqrt_d * kPreScale) : 0.0f;
+          const float vn = valid ? __half2float(__ushort_as_half(nrm[kTile])) * inv_sqrt_d : 0.0f;
+          S.norm[j & 3][1][t] = vn * kPreScale;
+          S.norm[j & 3][2][t] = share_log2(vn);
         }
         tc::fence_proxy_async_smem();
         tc::fence_before_sync();
@@ -405,6 +407,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
         const uint32_t tS = tb + kPreS + 128u * (j & 1) + lane_base + 64 * cw;
         const float4* kn = reinterpret_cast<const float4*>(S.norm[j & 3][0] + 64 * cw);
         const float4* vn = reinterpret_cast<const float4*>(S.norm[j & 3][1] + 64 * cw);
+        const float4* lv = reinterpret_cast<const float4*>(S.norm[j & 3][2] + 64 * cw);
+        const float2 qs2 = make_float2(qs, qs);
         const int left = a.len - (c_begin + j) * kChunkTokens - 64 * cw;   // tokens of the prefix from the first one on
         // logits over 2^e of 32 tokens: S times the keys' norms, -inf past the prefix
         auto logits = [&](int c0, float2 (&x)[16]) {
@@ -435,9 +439,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
             float2 x[16];
             logits(c0, x);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) m4[i & 3] = fmaxf(m4[i & 3], fmaxf(x[i].x, x[i].y));
+            for (int i = 0; i < 16; i += 2) {
+              const float4 f = lv[(c0 >> 2) + (i >> 1)];
+              const float2 y0 = fma2(x[i], qs2, make_float2(f.x, f.y)), y1 = fma2(x[i + 1], qs2, make_float2(f.z, f.w));
+              m4[i & 2] = fmaxf(m4[i & 2], fmaxf(y0.x, y0.y));
+              m4[(i & 2) + 1] = fmaxf(m4[(i & 2) + 1], fmaxf(y1.x, y1.y));
+            }
           }
-          top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qs;
+          top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         }
         S.xch[j & 1][cw][t] = top;
         // a wait that gave up joins the barrier's vote, so that the warps stop as one
@@ -476,7 +485,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
             }
           }
           // P' of 32 tokens at a time, over the S columns just read
-          const float2 qs2 = make_float2(qs, qs), nM = make_float2(-M, -M);
+          const float2 nM = make_float2(-M, -M);
           float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int g0 = 0; g0 < 64; g0 += 32) {

@@ -1,0 +1,142 @@
+"""Paged attention against rows in 64 bits where a fixed scale would lose digits: small and mixed value
+norms, values of zero, queries with one coordinate far above the rest.
+
+One KV head and at most 148 * 128 positions: a share (of a warpgroup, or a prefix split) is one chunk, so the
+bounds below count one chunk's roundings."""
+import math
+
+import numpy as np
+import pytest
+
+from packed_cache_attention_b200 import kvq
+from tests.paged_util import LOG2E, Paged
+from tests.parity_util import host_f32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    kvq._check("kvq_init", kvq.lib().kvq_init())
+    return torch.device("cuda:0")
+
+
+def exact_rows(P, q, lens, prefix, used=None):
+    """Rows in 64 bits and a bound of an fp32 kernel's error, element by element.
+
+    A softmax weight is off by a relative e, in the numerator and in the sum, so an output by at most 2 e of
+    the weighted mean of |v|. e is: the logit's error times ln 2, with A the sum of |q k| in log2 units: the
+    pair of a query 2^-22 of each product, fp32 sums of 24 products cut off at 2^-23, the products with the
+    norm and the scale, 2^-24 each of A: below 2^-18 A (high and low sums one after the other: 2^-17 A); the
+    pair of a share 2^-22; a chunk's 16 products cut off at 2^-23: 2^-19; 2^x and row sums of a chunk 2^-19;
+    the merge of at most 148 shares by 16 warps and of those 2^-18: together below 2^-17. Shares below fp16's
+    normal range are off by 2^-38 of the largest share, times a centroid below 5."""
+    q = host_f32(q).astype(np.float64)
+    B, Hq, _ = q.shape
+    out, bound = np.zeros(q.shape), np.zeros(q.shape)
+    pk, pv = P.kv(P.prefix_np, prefix)
+    for b, n in enumerate(lens):
+        k, v = P.kv(P.table_np[b], n)
+        k, v = np.concatenate([pk, k], 1)[0], np.concatenate([pv, v], 1)[0]
+        z = (k @ q[b].T).T / math.sqrt(128.0)                             # [heads][tokens]
+        p = np.exp(z - z.max(1, keepdims=True))
+        total = p.sum(1, keepdims=True)
+        out[b] = p @ v / total
+        A = (np.abs(k) @ np.abs(q[b].T)).T.max(1) / math.sqrt(128.0) * LOG2E
+        e = A * math.log(2) * 2.0 ** -17 + 2.0 ** -17
+        largest = (p * np.abs(v).max(1)).max(1, keepdims=True)
+        bound[b] = 2 * e[:, None] * (p @ np.abs(v)) / total + 5 * p.shape[1] * 2.0 ** -38 * largest / total
+    return out, bound
+
+
+def check(got, want, bound, dtype):
+    import torch
+    f = torch.finfo(dtype)
+    g = host_f32(got).astype(np.float64)
+    assert np.isfinite(g).all()
+    lim = bound * (1 + f.eps) + f.eps / 2 * np.abs(want) + f.tiny * f.eps
+    err = np.abs(g - want)
+    assert (err <= lim).all(), (float((err / lim).max()), float(err.max()))
+
+
+def _pool(dev, seed, bits_k, bits_v, lens, prefix, scale_of):
+    """A pool whose token i of a sequence (or of the prefix) has values of scale scale_of(rng, tokens)[i]."""
+    import torch
+    P = Paged(dev, seed, 1, bits_k, bits_v, 64, lens, prefix=prefix)
+    keys = []
+    for n, table in [(prefix, P.prefix_pages[None].contiguous())] + [(n, P.table[b:b + 1].contiguous()) for b, n in enumerate(lens)]:
+        if n == 0:
+            keys.append(None)
+            continue
+        K, V = P.rows(n, torch.float32)
+        V = V * torch.from_numpy(scale_of(P.rng, n)).float().to(dev)[:, None, None]
+        P.append(K, V, [0], [0, n], table=table)
+        keys.append((K, V))
+    assert kvq.kvq_packed_status(P.pool) == 0
+    return P, keys
+
+
+@pytest.mark.parametrize("bits_k,bits_v,heads", [(3, 3, 8), (4, 8, 3), (8, 2, 4)])
+@pytest.mark.parametrize("scale", [1e3, 1.0, 1e-3, 1e-5, 2e-7])
+def test_outputs_do_not_depend_on_the_scale_of_the_values(dev, bits_k, bits_v, heads, scale):
+    """Equal logits (a zero query) and small ones, values of one scale: own pages, a prefix, both."""
+    import torch
+    lens, prefix = [2000, 1, 130], 4001
+    P, _ = _pool(dev, 60 + bits_v, bits_k, bits_v, lens, prefix, lambda rng, n: np.full(n, scale))
+    q = torch.randn((3, heads, 128), device=dev) * 0.02
+    q[0] = 0.0
+    for pre in (0, prefix):
+        want, bound = exact_rows(P, q, lens, pre)
+        for dt in (torch.float32, torch.bfloat16, torch.float16):
+            if dt == torch.float16 and scale == 1e3 and np.abs(want).max() > 6e4:
+                continue
+            check(P.decode(q, lens, pre, out_dtype=dt), want, bound, dt)
+
+
+@pytest.mark.parametrize("bits_k,bits_v,heads", [(3, 3, 8), (4, 8, 3), (8, 2, 4)])
+def test_value_norms_over_seven_decades(dev, bits_k, bits_v, heads):
+    """Every row's query is the direction of one key, whose value is the smallest of all, or zero: the output is
+    that small value, or what the other tokens add up to."""
+    import torch
+    lens, prefix = [1500, 40, 700], 3000
+    P, keys = _pool(dev, 70 + bits_v, bits_k, bits_v, lens, prefix, lambda rng, n: 10.0 ** rng.uniform(-6, 1, n))
+    spread = torch.randn((3, heads, 128), device=dev)
+    for pre in (0, prefix):
+        for sharp in (0.0, 12.0, 25.0):
+            q = spread * 0.3
+            for b in range(3):
+                K, V = keys[0] if pre and b < 2 else keys[b + 1]
+                at = torch.argsort(V[:, 0].norm(dim=1))[:heads]              # tokens of the smallest values
+                k = K[at, 0]
+                # the direction in which this key stands out: q . k = sharp sqrt(128), keys weighted by their spread
+                d = k / P.scale[0] ** 2
+                q[b] = q[b] + sharp * math.sqrt(128.0) * d / (d * k).sum(1, keepdim=True)
+            want, bound = exact_rows(P, q, lens, pre)
+            for dt in (torch.float32, torch.bfloat16):
+                check(P.decode(q, lens, pre, out_dtype=dt), want, bound, dt)
+
+
+def test_the_top_logit_has_a_value_of_zero(dev):
+    """A token that takes almost all weight and adds nothing: the output is what the others add, 2^-17 to 2^-58 of
+    their values."""
+    import torch
+    lens, prefix = [300, 60], 900
+    P = Paged(dev, 80, 1, 4, 4, 64, lens, prefix=prefix)
+    sink = []
+    for n, table in [(prefix, P.prefix_pages[None].contiguous())] + [(n, P.table[b:b + 1].contiguous()) for b, n in enumerate(lens)]:
+        K, V = P.rows(n, torch.float32)
+        V[n // 2] = 0.0
+        P.append(K, V, [0], [0, n], table=table)
+        sink.append(K[n // 2, 0])
+    for pre in (0, prefix):
+        for sharp in (12.0, 25.0, 40.0):
+            q = torch.randn((2, 8, 128), device=dev) * 0.05
+            for b in range(2):
+                k = sink[0] if pre else sink[b + 1]
+                d = k / P.scale[0] ** 2
+                q[b] += sharp * math.sqrt(128.0) * d / (d * k).sum()
+            want, bound = exact_rows(P, q, lens, pre)
+            check(P.decode(q, lens, pre), want, bound, torch.float32)
