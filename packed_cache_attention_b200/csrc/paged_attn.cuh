@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
     const int c = tid - 64, blk = al->plan_col_block[c];
     if (blk >= 0 && blk < kH && c < al->plan_k_cols) S.col_of[blk] = static_cast<int8_t>(c);
   } else if (tid >= 192 && tid < 192 + kH) {
-    S.dequant[tid - 192] = al->dequant[tid - 192] * (inv_sqrt_d * kLog2e);
+    S.dequant[tid - 192] = al->width[tid - 192] ? al->dequant[tid - 192] * (inv_sqrt_d * kLog2e) : 0.0f;
   } else if (tid == 256) {
     // (asked for before the header's fields are looked at, so one round trip brings everything)
     const uint64_t dg = paged_digest(a.pool, hkv), ad = __ldcg(reinterpret_cast<const unsigned long long*>(&al->digest));
@@ -405,8 +405,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
       const int len = __ldg(a.pg.seq_lens + b);
       const int c_first = x - cs[b];
       // -------------------------------------------------------------- Q' (16 threads a row)
-      // Row h: q * f_b * log2(e) / sqrt(d) * 2^-e, its largest |value| in [0.5, 1); B operand of S,
-      // K-major: element (n, k) at (k / 8) * 256 + (n / 8) * 128 + (n % 8) * 16 + (k % 8) * 2, k = 2 * column
+      // Row h: q * f_b * log2(e) / sqrt(d) by a power of two (query_scale); B operand of S, K-major: element (n, k) at (k / 8) * 256 + (n / 8) * 128 + (n % 8) * 16 + (k % 8) * 2, k = 2 * column
       // + half; n < 8 high parts, n >= 8 low parts. The last chunk's products have read the old one.
       {
         const int h = t >> 4, i4 = 4 * (t & 15);
@@ -422,15 +421,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
             v[4] = hi.x * f.x; v[5] = hi.y * f.y; v[6] = hi.z * f.z; v[7] = hi.w * f.w;
           });
         }
-        float mx = 0.0f;
+        uint32_t mx = 0u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[i]));
+        for (int i = 0; i < 8; ++i) mx = max(mx, abs_bits(v[i]));
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        int e = 0;
-        if (mx > 0.0f) frexpf(mx, &e);
-        e = max(e, -126);                                   // 2^-e stays finite
-        const float sc = ldexpf(1.0f, -e);
+        for (int o = 8; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        float back;
+        const float sc = query_scale(mx, back);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int c = S.col_of[i4 + i];
@@ -442,7 +439,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
           *reinterpret_cast<uint32_t*>(p) = h0 | (h1 << 16);
           *reinterpret_cast<uint32_t*>(p + 128) = l0 | (l1 << 16);
         }
-        if ((t & 15) == 0) S.qscale[g][h] = ldexpf(1.0f, e);
+        if ((t & 15) == 0) S.qscale[g][h] = back;
         tc::fence_proxy_async_smem();
         named_sync(1 + g, 128);
       }

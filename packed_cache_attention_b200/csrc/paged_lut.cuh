@@ -210,6 +210,21 @@ __device__ __forceinline__ const uint8_t* paged_record(const uint8_t* pool, cons
   return pool + a.hdr_bytes + ((static_cast<size_t>(page) * a.n_kv_heads + hkv) * a.page_tiles + in) * a.rec_bytes;
 }
 
+// Scale of a row of Q' from the largest bits of its |values|: its largest value comes to [2^13, 2^14), so that
+// the low parts of its fp16 pairs end at 2^-38 of it (scaled to [0.5, 1) they ended at 2^-25, and a logit
+// had 22 bits). A block without key bits counts as 0 there, as its keys do. `back` undoes the scale; it is
+// NaN, and with it the row's logits, if a query value is not finite, in a block without key bits too
+// (inf * 0). Exponents stay where both scales are normal numbers.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+__device__ __forceinline__ float query_scale(uint32_t max_bits, float& back) {
+  const bool finite = max_bits < 0x7f800000u;
+  int e = 0;
+  if (finite && max_bits > 0) frexpf(__uint_as_float(max_bits), &e);
+  e = max(e, -111) - 14;
+  back = finite ? ldexpf(1.0f, e) : __int_as_float(0x7fc00000);
+  return ldexpf(1.0f, -e);
+}
+
 // Elements i .. i + 3 of a row of 16-bit or fp32 values (i a multiple of 4, rows 16-byte aligned).
 template <int DT>
 __device__ __forceinline__ float4 load4(const void* p, int64_t i) {

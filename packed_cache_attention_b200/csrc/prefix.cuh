@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
     const int blk = al->plan_col_block[tid - 64];
     S.col_block[tid - 64] = static_cast<int8_t>(blk < kH ? blk : -1);
   } else if (tid >= 192 && tid < 192 + kH) {
-    S.dequant[tid - 192] = al->dequant[tid - 192] * (inv_sqrt_d * kLog2e);
+    S.dequant[tid - 192] = al->width[tid - 192] ? al->dequant[tid - 192] * (inv_sqrt_d * kLog2e) : 0.0f;
   } else if (tid == 256) {
     // (asked for before the header's fields are looked at, so one round trip brings everything)
     const uint64_t dg = paged_digest(a.pool, hkv), ad = __ldcg(reinterpret_cast<const unsigned long long*>(&al->digest));
@@ -277,8 +277,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
     const int t = 32 * q + lane;                            // row of S and O, token of Khat, dim of Vhat
     const bool live = 32 * q < rows;                        // some row of the warp is a query
     // -------------------------------------------------------------- Q'
-    // Row r: q * f_b * log2(e) / sqrt(d) * 2^-e, its largest |value| in [0.5, 1). The rows are
-    // staged in fp32 and taken up by row: columns 24 wg .. 24 wg + 23 of row t.
+    // Row r: q * f_b * log2(e) / sqrt(d) by a power of two (query_scale). The rows are staged in fp32 and
+    // taken up by row: columns 24 wg .. 24 wg + 23 of row t.
     float* stg = reinterpret_cast<float*>(sm + kPreKOff);
     by_dtype(a.q_dtype, [&](auto dt) {
       float4 v[kPreRows / 16];                              // (all rows' loads are in flight together)
@@ -305,18 +305,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
     named_sync(1, 512);
     // (rows past the batch come up to the warp's end as zeros; a warp of such rows alone takes no part: what its
     // rows of Q', S and O hold concerns no other row)
-    float mx = 0.0f;
+    uint32_t mx = 0u;
     if (live) {
 #pragma unroll 8
-      for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(stg[t * kPreQPitch + 32 * wg + i]));
+      for (int i = 0; i < 32; ++i) mx = max(mx, abs_bits(stg[t * kPreQPitch + 32 * wg + i]));
     }
-    S.xch[wg >> 1][wg & 1][t] = mx;
+    S.xch[wg >> 1][wg & 1][t] = __uint_as_float(mx);
     named_sync(1, 512);
-    mx = fmaxf(fmaxf(S.xch[0][0][t], S.xch[0][1][t]), fmaxf(S.xch[1][0][t], S.xch[1][1][t]));
-    int e = 0;
-    if (mx > 0.0f) frexpf(mx, &e);
-    e = max(e, -126);                                       // 2^-e stays finite
-    const float sc = ldexpf(1.0f, -e), qs = ldexpf(1.0f, e);
+    mx = max(max(abs_bits(S.xch[0][0][t]), abs_bits(S.xch[0][1][t])), max(abs_bits(S.xch[1][0][t]), abs_bits(S.xch[1][1][t])));
+    float qs;
+    const float sc = query_scale(mx, qs);
 #pragma unroll
     for (int c8 = 0; c8 < 24; c8 += 8) {
       if (!live) break;

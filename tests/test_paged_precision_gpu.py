@@ -140,3 +140,62 @@ def test_the_top_logit_has_a_value_of_zero(dev):
                 q[b] += sharp * math.sqrt(128.0) * d / (d * k).sum()
             want, bound = exact_rows(P, q, lens, pre)
             check(P.decode(q, lens, pre), want, bound, torch.float32)
+
+
+def _no_bits(P):
+    """Blocks of the head without key bits."""
+    w = np.asarray(P.ref["w"])[0]
+    assert (w == 0).any()
+    return np.flatnonzero(w == 0)
+
+
+@pytest.mark.parametrize("bits_k,heads", [(1, 8), (2, 3)])
+@pytest.mark.parametrize("power", [10, 16, 40, 100])
+def test_a_coordinate_without_key_bits_does_not_cost_the_others_digits(dev, bits_k, heads, power):
+    """Queries 2^power times larger in a block whose keys are stored as zero: the logits do not see it."""
+    import torch
+    lens, prefix = [500, 1, 60], 700
+    P, _ = _pool(dev, 90 + bits_k, bits_k, 3, lens, prefix, lambda rng, n: np.ones(n))
+    b = int(_no_bits(P)[0])
+    for dt in (torch.float32, torch.bfloat16):
+        q = (torch.randn((3, heads, 128), device=dev) / P.scale[0]).to(dt)
+        big = q.clone()
+        big[..., [b, b + 64]] = 2.0 ** power
+        for pre in (0, prefix):
+            want, bound = exact_rows(P, q, lens, pre)
+            check(P.decode(big, lens, pre), want, bound, torch.float32)
+
+
+def test_a_query_that_is_not_finite_in_a_block_without_key_bits(dev):
+    """0 * inf and 0 * NaN: the row is NaN, the other rows are as they were."""
+    import torch
+    lens, prefix = [200, 40, 0], 300
+    P, _ = _pool(dev, 95, 1, 3, lens, prefix, lambda rng, n: np.ones(n))
+    b = int(_no_bits(P)[-1])
+    q = torch.randn((3, 8, 128), device=dev)
+    bad = torch.zeros((3, 8), dtype=torch.bool, device=dev)
+    odd = q.clone()
+    odd[0, 1, b], odd[1, 7, b + 64], odd[1, 2, b] = float("inf"), float("nan"), -float("inf")
+    bad[0, 1] = bad[1, 7] = bad[1, 2] = True
+    for pre in (0, prefix):
+        got, want = P.decode(odd, lens, pre), P.decode(q, lens, pre)
+        assert bool(got[bad].isnan().all()) and torch.equal(got[~bad], want[~bad])
+
+
+def test_queries_at_the_ends_of_the_fp32_range(dev):
+    """Largest and smallest queries, whose logits are one token's, or nothing."""
+    import torch
+    lens, prefix = [150, 90], 200
+    P, _ = _pool(dev, 96, 3, 3, lens, prefix, lambda rng, n: np.ones(n))
+    for size in (3e38, 1e30, 1e-30, 1e-38, 1e-45):
+        q = torch.full((2, 8, 128), size, device=dev)
+        for pre in (0, prefix):
+            want, bound = exact_rows(P, q, lens, pre)
+            got = P.decode(q, lens, pre)
+            if size < 1:
+                check(got, want, bound, torch.float32)
+                continue
+            # one token has all the weight: its value, or NaN where the logits pass fp32
+            g = host_f32(got)
+            right = np.isclose(g, want, rtol=2.0 ** -20, atol=0).all(2)
+            assert right.all() if size == 1e30 else (right | np.isnan(g).all(2)).all()
