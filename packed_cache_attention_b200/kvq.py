@@ -520,10 +520,22 @@ def _rows(t) -> Tensor4:
     return Tensor4(sh[0], sh[1], sh[2], sh[3], st[0], st[1], st[2], _code_of(t.dtype), 0)
 
 
+def _axis_bytes(axis) -> bytes:
+    """64 axis numbers as bytes. (bytes() of an array would give its memory, not its numbers.)"""
+    if not isinstance(axis, (list, tuple, bytes)):
+        axis = axis.tolist() if hasattr(axis, "tolist") else list(axis)
+    if len(axis) != 64:
+        raise ValueError("axis needs 64 entries")
+    try:
+        return bytes(axis)
+    except (TypeError, ValueError):
+        raise ValueError("axis needs whole numbers from 0 on") from None
+
+
 def rope_desc(table, positions, axis=None) -> RopeDesc:
     """Rotation of block b by the angle of position positions[axis[b]][token]: table fp32
     [n_positions][64][2] of (cos, sin), positions int32 [n_axes][tokens] (or [tokens] for one axis), axis a
-    sequence of 64 axis numbers (None: all 0). Keeps the tensors alive."""
+    sequence, array or tensor of 64 axis numbers (None: all 0). Keeps the tensors alive."""
     sh = table.shape
     if len(sh) != 3 or sh[1] != 64 or sh[2] != 2 or table.dtype is not _torch().float32 or not table.is_contiguous():
         raise ValueError("table must be contiguous fp32 [n_positions][64][2]")
@@ -533,9 +545,7 @@ def rope_desc(table, positions, axis=None) -> RopeDesc:
     n_axes, n_tokens = positions.shape
     r = RopeDesc(table.data_ptr(), at, positions.stride(0), sh[0], n_axes)
     if axis is not None:
-        if len(axis) != 64:
-            raise ValueError("axis needs 64 entries")
-        ctypes.memmove(ctypes.addressof(r) + _AXIS_AT, bytes(axis), 64)
+        ctypes.memmove(ctypes.addressof(r) + _AXIS_AT, _axis_bytes(axis), 64)
     r.tensors, r.n_tokens = (table, positions), n_tokens
     return r
 

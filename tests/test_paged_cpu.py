@@ -216,3 +216,23 @@ def test_every_split_rule_covers_the_batch():
             for i in range(s):
                 assert (i + 1) * int(c) // s > i * int(c) // s
         assert math.isfinite(best)
+
+
+def test_axis_maps_of_every_kind_are_their_numbers():
+    """Lists, tuples, bytes, numpy and torch integers of any width, strided ones: the same 64 bytes."""
+    import array
+
+    import torch
+    table, pos = torch.from_numpy(angle_table(4)), torch.zeros((4, 5), dtype=torch.int32)
+    want = np.minimum((np.arange(64) + 8) // 24, 2)
+    kinds = [want.tolist(), tuple(want.tolist()), bytes(want.tolist()), bytearray(want.tolist()), [np.int32(a) for a in want],
+             array.array("i", want.tolist()), array.array("q", want.tolist()), range(64)]
+    kinds += [want.astype(t) for t in (np.uint8, np.int8, np.int16, np.int32, np.int64, np.uint64)]
+    kinds += [np.repeat(want.astype(np.int32), 2)[::2], torch.from_numpy(want), torch.from_numpy(want).int(), torch.from_numpy(want).to(torch.uint8)]
+    for axis in kinds:
+        r = kvq.rope_desc(table, pos, axis)
+        assert bytes(r.axis) == bytes(range(64)) if isinstance(axis, range) else list(r.axis) == want.tolist(), type(axis)
+    for bad in (want.astype(np.float32), want[:63], [0] * 65, [-1] * 64, [256] * 64, [[0]] * 64, "0" * 64, want.reshape(64, 1),
+                torch.from_numpy(want).float()):
+        with pytest.raises(ValueError):
+            kvq.rope_desc(table, pos, bad)
