@@ -359,7 +359,9 @@ __global__ void __launch_bounds__(QTile<DT>::kWarps * 32, 1) kvq_paged_quant(con
   {
     unsigned code = (threadIdx.x == 0) ? paged_header_code<true>(p.pool, a) : 0u;
     for (int h = threadIdx.x; h < a.n_kv_heads; h += blockDim.x)
-      if (paged_digest(p.pool, h) != p.alloc[h].digest) code = KVQ_ERR_MISMATCH;
+      // (the digest does not cover the budget: a pool may have been given an allocation of another one)
+      if ((paged_digest(p.pool, h) != p.alloc[h].digest) | (p.alloc[h].bits_k != a.bits_k) | (p.alloc[h].k_words != a.bits_k * kD))
+        code = KVQ_ERR_MISMATCH;
     if (code) atomicCAS(&sCode, 0u, code);
   }
   // Tiles per sequence. A sequence whose rows or positions do not fit gets none.
@@ -464,14 +466,14 @@ __global__ void __launch_bounds__(QTile<DT>::kWarps * 32, 1) kvq_paged_quant(con
         }
         sEnt[i] = e;
       }
-      n_cls = al->k_words == k_words ? min(max(al->n_classes, 0), 8) : -1;   // -1: made for another budget
+      n_cls = min(max(al->n_classes, 0), 8);
       if (lane < 8)
         sCls[lane] = static_cast<uint32_t>(al->class_width[lane]) | (static_cast<uint32_t>(al->class_first[lane]) << 8) |
                      (static_cast<uint32_t>(al->class_blocks[lane]) << 16);
       __syncwarp();
       cur_h = cur.h;
     }
-    const bool write = cur.rec != nullptr && n_cls >= 0, by_rows = few(cur);
+    const bool write = cur.rec != nullptr, by_rows = few(cur);
     if (by_rows && write) {
       const int64_t es = sizeof(T);
       if (append_few<DT, BVT>(p.K + es * (cur.h * p.ksh + cur.tok0 * p.kst), p.V + es * (cur.h * p.vsh + cur.tok0 * p.vst),

@@ -247,6 +247,29 @@ def test_a_call_with_another_allocation_or_shape_writes_nothing(dev):
             assert kvq.kvq_workspace_status(ws) == kvq.KVQ_ERR_MISMATCH and bool((out == 7.0).all())
 
 
+@pytest.mark.parametrize("tokens", [3, 40])
+def test_an_allocation_of_another_budget_is_reported_by_the_append(dev, tokens):
+    """A pool of 3 bits set up with an allocation of 2, for all heads or for one: MISMATCH, no record written."""
+    import torch
+    P = Paged(dev, 19, 2, 3, 3, 64, [100])
+    other = Paged(dev, 19, 2, 2, 3, 64, [100]).alloc
+    K, V = P.rows(tokens, torch.bfloat16)
+    for heads in (slice(0, 2), slice(0, 1), slice(1, 2)):
+        alloc = P.alloc.clone().view(2, -1)
+        alloc[heads] = other.view(2, -1)[heads]
+        alloc = alloc.flatten()
+        pool = P.pool.clone()
+        kvq.kvq_paged_init(alloc, P.desc, pool)
+        before = pool.clone()
+        kvq.kvq_paged_append(K, V, alloc, P.desc, P.table, P.ints([0]), P.ints([0, tokens]), pool)
+        assert kvq.kvq_packed_status(pool) == kvq.KVQ_ERR_MISMATCH
+        assert torch.equal(before[P.hdr:], pool[P.hdr:])
+        ws = kvq.kvq_paged_decode_workspace(P.desc, 1, 8)
+        out = torch.full((1, 8, 128), 7.0, device=dev)
+        kvq.kvq_paged_decode_attn(torch.randn((1, 8, 128), device=dev), pool, alloc, P.desc, P.table, P.ints([tokens]), ws=ws, out=out)
+        assert kvq.kvq_workspace_status(ws) == kvq.KVQ_ERR_MISMATCH and bool((out == 7.0).all())
+
+
 # ------------------------------------------------------------------------------ decode
 
 LENS = [0, 1, 31, 33, 128, 129, 700, 0]
