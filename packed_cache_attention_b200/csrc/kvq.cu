@@ -1058,10 +1058,10 @@ PrefixPlan prefix_plan(int n_rows, int n_kv_heads) {
   return p;
 }
 
-// Workspace: status word, the plan that the decode leaves to the merge, (m, l, O) of the
+// Workspace: status word, the plan and the refused heads that the decode leaves to the merge, (m, l, O) of the
 // sequences' own shares, then of the prefix's.
 struct PagedWs {
-  size_t plan, own_m, own_l, own_o, pre_m, pre_l, pre_o, total;
+  size_t plan, refused, own_m, own_l, own_o, pre_m, pre_l, pre_o, total;
 };
 PagedWs paged_ws(int batch, int n_kv_heads, int group, bool prefix) {
   PagedWs w;
@@ -1072,7 +1072,8 @@ PagedWs paged_ws(int batch, int n_kv_heads, int group, bool prefix) {
     pre = static_cast<size_t>(p.splits) * n_kv_heads * p.groups * kPreRows;
   }
   w.plan = sizeof(WsHeader);
-  w.own_m = align_up(w.plan + sizeof(int2) * (batch + 1), 128);
+  w.refused = w.plan + sizeof(int2) * (batch + 1);
+  w.own_m = align_up(w.refused + sizeof(int) * n_kv_heads, 128);
   w.own_l = align_up(w.own_m + 4 * own, 128);
   w.own_o = align_up(w.own_l + 4 * 4 * own, 128);
   w.pre_m = align_up(w.own_o + 4 * kD * own, 128);
@@ -1255,6 +1256,7 @@ kvq_status kvq_paged_decode_attn(const void* q, const kvq_tensor4* qd, const voi
   m.group = group;
   m.batch = seqs->batch;
   m.plan = reinterpret_cast<const int2*>(w8 + w.plan);
+  m.refused = reinterpret_cast<const int*>(w8 + w.refused);
   m.ctas = paged_ctas(d->n_kv_heads);
   m.entries = 4 * m.ctas + seqs->batch;
   m.own_m = reinterpret_cast<const float*>(w8 + w.own_m);
@@ -1309,6 +1311,7 @@ kvq_status kvq_paged_decode_attn(const void* q, const kvq_tensor4* qd, const voi
   a.part_l = reinterpret_cast<float*>(w8 + w.own_l);
   a.part_o = reinterpret_cast<float*>(w8 + w.own_o);
   a.plan = reinterpret_cast<int2*>(w8 + w.plan);
+  a.refused = reinterpret_cast<int*>(w8 + w.refused);
   a.status = reinterpret_cast<unsigned*>(w8);
   a.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
   a.debug_no_loads = g_debug_no_loads.load(std::memory_order_relaxed);

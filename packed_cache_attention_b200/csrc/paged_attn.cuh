@@ -45,7 +45,8 @@ struct PagedAttn {
   float* part_l;                          // [head][entry][4 quarters][8]
   float* part_o;                          // [head][entry][8][128]
   int2* plan;                             // [batch + 1]: first chunk and chunks of a sequence (-1: not decoded);
-                                          // then all chunks and the warpgroups that share them
+                                          // then all chunks
+  int* refused;                           // [head]: its header or allocation does not fit, its rows stay as they are
   unsigned* status;
   uint32_t wait_limit;
   int debug_no_loads;
@@ -248,7 +249,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
   __syncthreads();
   tc::fence_after_sync();
   const bool bad = S.bad != 0;
-  if (blockIdx.x == 0 && tid < a.pg.batch) a.plan[tid] = make_int2(mine.at, bad ? -1 : mine.n);
+  if (blockIdx.x == 0 && tid < a.pg.batch) a.plan[tid] = make_int2(mine.at, mine.n);
+  if (cta == 0 && tid == 0) a.refused[hkv] = bad;
   const uint32_t tbase = S.tmem_base + 128u * g;            // K-hat 96 (V-hat^T in 64 of them), S 16, O 16
   const uint32_t tS = tbase + 96, tO = tbase + 112;
   const Shares sh(chunks, a.ctas);
@@ -686,6 +688,7 @@ struct MergeArgs {
   void* out;
   int out_dtype, n_q_heads, n_kv_heads, group, batch;
   const int2* plan;
+  const int* refused;
   int entries, ctas;
   const float *own_m, *own_l, *own_o;      // as PagedAttn's part_*
   int prefix_len, pre_groups, pre_splits;
@@ -709,7 +712,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kvq_paged_merge(const MergeA
   const int hkv = hq / a.group, h = hq - hkv * a.group;
   grid_dependency_wait();
   const int2 plan = __ldcg(a.plan + b), all = __ldcg(a.plan + a.batch);
-  if (plan.y < 0) return;                                    // refused
+  const int refused = __ldcg(a.refused + hkv);
+  if (plan.y < 0 || refused) return;
   // own shares: workers w0 .. of the first CTAs one by one, CTAs c_lo .. c_hi - 1 whose workers all
   // lie in the sequence by their first, the rest one by one
   const Shares sh(all.x, a.ctas);

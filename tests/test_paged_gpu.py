@@ -425,6 +425,40 @@ def test_one_heads_allocation_swapped(dev):
         check_rows(out[:, :4], want[:, :4], bound[:, :4], torch.float32)
 
 
+@pytest.mark.parametrize("batch,head", [(3, 0), (3, 1), (700, 0), (700, 1), (700, None)])
+def test_a_refused_head_keeps_its_rows_and_no_others(dev, batch, head):
+    """Whichever head's allocation differs (None: the pool's shape), its rows stay as they were, those of empty
+    sequences and of the batch's end too; the other head's are right."""
+    import torch
+    lens = ([40, 0, 130] * 234)[:batch]
+    P = Paged(dev, 24, 2, 3, 3, 64, lens, prefix=70)
+    P.fill(lens, torch.bfloat16, prefix=70)
+    other = Paged(dev, 15, 2, 3, 3, 64, [64]).alloc
+    alloc = P.alloc.clone().view(2, -1)
+    desc = P.desc
+    if head is None:
+        desc = kvq.paged_desc(P.desc.n_pages - 1, 64, 2, 3, 3)
+    else:
+        alloc[head] = other.view(2, -1)[head]
+    q = torch.randn((batch, 4, 128), device=dev)
+    for prefix in (0, 70):
+        want = P.decode(q, lens, prefix)
+        ws = kvq.kvq_paged_decode_workspace(desc, batch, 4, prefix)
+        out = torch.full((batch, 4, 128), 7.0, device=dev)
+        kvq.kvq_paged_decode_attn(q, P.pool, alloc.flatten(), desc, P.table, P.ints(lens), prefix_pages=P.prefix_pages,
+                                  prefix_len=prefix, ws=ws, out=out)
+        assert kvq.kvq_workspace_status(ws) == kvq.KVQ_ERR_MISMATCH
+        for h in range(2):
+            rows = slice(2 * h, 2 * h + 2)
+            if head is None or h == head:
+                assert bool((out[:, rows] == 7.0).all())
+            else:
+                assert torch.equal(out[:, rows], want[:, rows])
+        kvq.kvq_workspace_init(ws)
+        again = kvq.kvq_paged_decode_attn(q, P.pool, P.alloc, P.desc, P.table, P.ints(lens), prefix_pages=P.prefix_pages, prefix_len=prefix, ws=ws)
+        assert torch.equal(again, want) and kvq.kvq_workspace_status(ws) == 0
+
+
 def test_calls_on_a_given_stream_without_buffers(dev):
     """Outputs and workspaces that a call makes belong to the stream it was given."""
     import torch
