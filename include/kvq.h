@@ -452,7 +452,8 @@ typedef struct {
   const int32_t* seq_lens;   /* [batch] positions stored (append: before the call) */
   int64_t table_stride;
   int32_t batch;
-  int32_t max_pages;         /* entries of a table row that may be read */
+  int32_t max_pages;         /* entries of a table row that may be read; max_pages * page_tokens < 2^31 - 4096,
+                              * times batch at most 2^35 (KVQ_ERR_RANGE) */
 } kvq_page_table;
 
 /* Bytes of a pool: a header of kvq_packed_header_bytes(n_kv_heads) bytes, then n_pages pages

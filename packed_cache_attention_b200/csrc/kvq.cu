@@ -953,6 +953,8 @@ bool rows_apart(const kvq_tensor4* t) {
 
 // Positions are 32-bit, with room for a chunk to be rounded up.
 constexpr long long kMaxPositions = 0x7fffffffLL - 4096;
+// Positions of all sequences of a call together: a batch's tiles and chunks are counted in 32 bits.
+constexpr long long kMaxBatchPositions = 1LL << 35;
 
 bool paged_ok(const kvq_paged_desc* d) {
   return d && d->n_pages >= 1 && d->page_tokens >= kTile && d->page_tokens % kTile == 0 && d->page_tokens <= 65536 &&
@@ -973,7 +975,8 @@ kvq_status paged_args(const kvq_paged_desc* d, const kvq_page_table* s, PagedArg
     if (!s->block_table || !s->seq_lens) return KVQ_ERR_ARG;
     if (s->batch < 1 || s->batch > kPagedMaxBatch || s->max_pages < 1) return KVQ_ERR_SHAPE;
     if (s->batch > 1 && s->table_stride < s->max_pages) return KVQ_ERR_ARG;
-    if (static_cast<long long>(s->max_pages) * d->page_tokens > kMaxPositions) return KVQ_ERR_RANGE;
+    const long long positions = static_cast<long long>(s->max_pages) * d->page_tokens;
+    if (positions > kMaxPositions || positions * s->batch > kMaxBatchPositions) return KVQ_ERR_RANGE;
     a.block_table = s->block_table;
     a.seq_lens = s->seq_lens;
     a.table_stride = s->table_stride;

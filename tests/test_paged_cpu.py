@@ -236,3 +236,16 @@ def test_axis_maps_of_every_kind_are_their_numbers():
                 torch.from_numpy(want).float()):
         with pytest.raises(ValueError):
             kvq.rope_desc(table, pos, bad)
+
+
+@pytest.mark.parametrize("batch,max_pages", [(1024, (1 << 19) + 1), (17, (1 << 25) - 65), (2, 1 << 25)])
+def test_batches_whose_tiles_do_not_fit_32_bits_are_refused(L, batch, max_pages):
+    """max_pages * 64 * batch past 2^35 (or a sequence past 2^31 - 4096 positions), by append and decode."""
+    mem, ws = buf(), buf(WS_BYTES)
+    seqs = _pages(mem, batch=batch, max_pages=max_pages)
+    kd = _t4(T=10)
+    assert L.kvq_paged_append(mem, ctypes.byref(kd), mem, ctypes.byref(kd), None, mem, ctypes.byref(D), ctypes.byref(seqs), mem, mem,
+                              None) == RANGE
+    qd = kvq.Tensor4(batch, 16, 1, 128, 2048, 128, 128, kvq.KVQ_BF16, 0)
+    assert L.kvq_paged_decode_attn(mem, ctypes.byref(qd), mem, mem, ctypes.byref(D), ctypes.byref(seqs), None, mem, 0, ws, WS_BYTES,
+                                   None) == RANGE
