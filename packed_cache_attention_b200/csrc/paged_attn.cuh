@@ -10,8 +10,7 @@
 // sequence but a chunk: per KV head, all chunks of the batch form one list, cut into equal
 // contiguous ranges, one per warpgroup (4 per CTA, one CTA per SM). A warpgroup walks the
 // sequences of its range, building Q' anew for each, and leaves one (m, l, O) per sequence it
-// met. Warpgroup w of the list and sequence b share entry w + b: along the list either w or b grows,
-// so no two pairs meet. The fewest warpgroups that keep the longest range are used, spread over
+// met (paged_split.h). The fewest warpgroups that keep the longest range are used, spread over
 // the SMs; those of a CTA that all lie in one sequence join their results first. One CTA per
 // (sequence, head) instead took 217 us on 32 sequences of 64 to 16384 tokens, where the longest
 // sequence set the time; this split takes 92 us.
@@ -92,19 +91,6 @@ struct Ring {
       parity ^= 1u;
     }
   }
-};
-
-// The 4 * ctas warpgroups of a head share `chunks` chunks, `per` each (the last one what is left):
-// as few as keep the longest range. (32-bit divisions: 64-bit ones took 1 us of a call.)
-struct Shares {
-  int per, workers, per_cta, chunks;        // chunks of a worker, workers, workers of a CTA (consecutive ranges)
-  __device__ __forceinline__ Shares(int chunks, int ctas) : chunks(chunks) {
-    per = max(1, (chunks + 4 * ctas - 1) / (4 * ctas));
-    workers = (chunks + per - 1) / per;
-    per_cta = max(1, (workers + ctas - 1) / ctas);
-  }
-  __device__ __forceinline__ int first(int w) const { return min(w * per, chunks); }   // first chunk of worker w
-  __device__ __forceinline__ int of(int x) const { return x / per; }                   // worker of chunk x
 };
 
 // Shares the batch out: chunk offsets of the sequences to `cs` (batch + 1 entries); `len` is that of
@@ -254,13 +240,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) kvq_paged_gtq(const PagedAttn 
   const uint32_t tbase = S.tmem_base + 128u * g;            // K-hat 96 (V-hat^T in 64 of them), S 16, O 16
   const uint32_t tS = tbase + 96, tO = tbase + 112;
   const Shares sh(chunks, a.ctas);
-  const int w_cta = cta * sh.per_cta, w_end = min(w_cta + sh.per_cta, sh.workers);   // this CTA's workers
+  const CtaShare mine_cta(sh, cs, a.pg.batch, cta);         // this CTA's workers
+  const int w_cta = mine_cta.w, w_end = mine_cta.w_end, b_cta = mine_cta.b;
+  const bool joint = mine_cta.joint;
   const int w = g < sh.per_cta ? w_cta + g : sh.workers;
   const int x0 = w < sh.workers ? sh.first(w) : 0, x1 = w < sh.workers ? sh.first(w + 1) : 0;
   const int b0 = x1 > x0 ? find_span(cs, a.pg.batch, x0) : 0;
-  // several workers inside one sequence leave one share, at the first one's entry
-  const int b_cta = w_cta + 1 < w_end ? find_span(cs, a.pg.batch, sh.first(w_cta)) : 0;
-  const bool joint = w_cta + 1 < w_end && sh.first(w_end) <= cs[b_cta + 1];
   volatile int* abort_flag = &S.wg_abort[g];
   const size_t e0 = static_cast<size_t>(hkv) * a.entries + w;   // entry of sequence b: e0 + b
 
@@ -714,28 +699,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kvq_paged_merge(const MergeA
   const int2 plan = __ldcg(a.plan + b), all = __ldcg(a.plan + a.batch);
   const int refused = __ldcg(a.refused + hkv);
   if (plan.y < 0 || refused) return;
-  // own shares: workers w0 .. of the first CTAs one by one, CTAs c_lo .. c_hi - 1 whose workers all
-  // lie in the sequence by their first, the rest one by one
-  const Shares sh(all.x, a.ctas);
-  const int per = sh.per_cta;
-  int w0 = 0, n_own = 0, n_lo = 0, n_mid = 0, w_mid = 0;
-  if (plan.y > 0) {
-    w0 = sh.of(plan.x);
-    const int w_end = sh.of(plan.x + plan.y - 1) + 1;
-    int c_lo = w0 / per, c_hi = (w_end + per - 1) / per;
-    if (sh.first(c_lo * per) < plan.x) ++c_lo;
-    if (sh.first(min(c_hi * per, sh.workers)) > plan.x + plan.y) --c_hi;
-    n_mid = max(0, c_hi - c_lo);
-    if (n_mid > 0) {
-      w_mid = c_lo * per;
-      n_lo = w_mid - w0;
-      n_own = n_lo + n_mid + max(0, w_end - c_hi * per);
-    } else {
-      n_lo = n_own = w_end - w0;
-    }
-  }
+  const OwnShares own(Shares(all.x, a.ctas), plan.x, plan.y);
   const int n_pre = a.prefix_len > 0 ? a.pre_splits : 0;
-  const int n = n_pre + n_own;
+  const int n = n_pre + own.n;
   const int row = b * a.group + h, rg = row / kPreRows, r = row - rg * kPreRows;
   float M = -INFINITY, L = 0.0f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -756,9 +722,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kvq_paged_merge(const MergeA
         lv[u] = __ldcg(a.pre_l + e);
         ov[u] = __ldcg(reinterpret_cast<const float4*>(a.pre_o + e * kD) + lane);
       } else if (i < n) {
-        const int k = i - n_pre;
-        const int w = k < n_lo ? w0 + k : k < n_lo + n_mid ? w_mid + (k - n_lo) * per : w_mid + n_mid * per + (k - n_lo - n_mid);
-        const size_t e = static_cast<size_t>(hkv) * a.entries + w + b;
+        const size_t e = static_cast<size_t>(hkv) * a.entries + own.worker(i - n_pre) + b;
         mv[u] = __ldcg(a.own_m + e * 8 + h);
         const float* l = a.own_l + e * 32 + h;
         lv[u] = (__ldcg(l) + __ldcg(l + 8)) + (__ldcg(l + 16) + __ldcg(l + 24));

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "paged_split.h"
 
 namespace kvq {
 
@@ -58,17 +59,6 @@ __device__ __forceinline__ int block_exclusive(int v, int* part, int n_warps, in
   }
   __syncthreads();
   return before + inc - v;
-}
-
-// Largest i with start[i] <= x, start ascending over n + 1 entries, start[0] <= x < start[n].
-__device__ __forceinline__ int find_span(const int* start, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  return lo;
 }
 
 }  // namespace kvq

@@ -249,3 +249,93 @@ def test_batches_whose_tiles_do_not_fit_32_bits_are_refused(L, batch, max_pages)
     qd = kvq.Tensor4(batch, 16, 1, 128, 2048, 128, 128, kvq.KVQ_BF16, 0)
     assert L.kvq_paged_decode_attn(mem, ctypes.byref(qd), mem, mem, ctypes.byref(D), ctypes.byref(seqs), None, mem, 0, ws, WS_BYTES,
                                    None) == RANGE
+
+
+SPLIT_SOURCE = r"""
+#include "paged_split.h"
+#include <vector>
+using namespace kvq;
+
+// One head's decode of a list (cs: chunk offsets of the sequences): every share it leaves, as the
+// kernel's warpgroups walk their ranges, in `put(entry, sequence, first chunk, chunks)`; then the shares that the
+// merge reads for every sequence. Returns 0, or the number of the first thing that does not fit.
+extern "C" int split(int batch, const int* cs, int ctas, long long* shares) {
+  const int chunks = cs[batch], entries = 4 * ctas + batch;
+  const Shares sh(chunks, ctas);
+  struct Left { int b, n, times; };
+  std::vector<Left> left(entries, Left{-1, 0, 0});
+  int walked = 0;
+  for (int cta = 0; cta < ctas; ++cta) {
+    const CtaShare c(sh, cs, batch, cta);
+    if (c.w_end - c.w > 4) return 1;                        // a warpgroup has one range
+    for (int g = 0; g < 4 && g < sh.per_cta; ++g) {
+      const int w = c.w + g;
+      int x = w < sh.workers ? sh.first(w) : 0;
+      const int x1 = w < sh.workers ? sh.first(w + 1) : 0;
+      if (w < sh.workers && x1 <= x) return 2;              // an empty range
+      if (x1 - x > sh.per) return 3;
+      int b = x1 > x ? find_span(cs, batch, x) : 0;
+      while (x < x1) {
+        const int n = (x1 < cs[b + 1] ? x1 : cs[b + 1]) - x;
+        if (n <= 0 || x < cs[b]) return 4;
+        const int e = c.joint ? c.w + c.b : w + b;
+        if (c.joint && b != c.b) return 5;
+        if (e < 0 || e >= entries) return 6;
+        if (left[e].b >= 0 && (left[e].b != b || !c.joint)) return 7;   // two shares at one entry
+        left[e].b = b;
+        left[e].n += n;
+        walked += n;
+        x += n;
+        if (x < x1) do ++b; while (cs[b + 1] == x);
+      }
+    }
+  }
+  if (walked != chunks) return 8;
+  *shares = 0;
+  for (int b = 0; b < batch; ++b) {
+    const OwnShares own(sh, cs[b], cs[b + 1] - cs[b]);
+    int n = 0;
+    for (int k = 0; k < own.n; ++k) {
+      const int e = own.worker(k) + b;
+      if (e < 0 || e >= entries || left[e].b != b || left[e].times++) return 9;   // not written, another's, or twice
+      n += left[e].n;
+    }
+    if (n != cs[b + 1] - cs[b]) return 10;                  // a share is missed
+    *shares += own.n;
+  }
+  for (const Left& l : left)
+    if (l.b >= 0 && l.times != 1) return 11;                // a share that nobody reads
+  return 0;
+}
+"""
+
+
+def test_decode_and_merge_agree_on_every_share(tmp_path):
+    """The functions that the kernels call, compiled for the host: for random batches (empty sequences, one long one,
+    more sequences than warpgroups) every chunk is walked once, no two shares have one entry, and the merge reads
+    each share of its sequence once and no other."""
+    import shutil
+    import subprocess
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no g++")
+    src, so = tmp_path / "split.cpp", tmp_path / "split.so"
+    src.write_text(SPLIT_SOURCE)
+    subprocess.run([gxx, "-std=c++17", "-O1", "-Wall", "-Werror", "-fsanitize=undefined", "-fno-sanitize-recover", "-shared", "-fPIC",
+                    "-static-libgcc", "-I", cc.ROOT + "/packed_cache_attention_b200/csrc", str(src), "-o", str(so)], check=True)
+    split = ctypes.CDLL(str(so)).split
+    rng = np.random.default_rng(2)
+    got = ctypes.c_longlong()
+    batches = [([0], 1), ([1], 148), ([0, 0, 0], 18), ([5, 0, 0, 7], 1), ([1 << 24], 148), ([4] * 148, 148), ([1] * 1024, 1),
+               ([0] * 500 + [3] + [0] * 523, 148), ([1 << 18] * 1024, 148)]
+    for _ in range(4000):
+        n = int(rng.integers(1, 1025)) if rng.random() < 0.1 else int(rng.integers(1, 20))
+        c = np.floor(np.exp(rng.uniform(0, np.log(rng.choice([3, 30, 3000])), n))).astype(int) * (rng.random(n) < rng.choice([0.3, 0.9, 1.0]))
+        batches.append((c.tolist(), int(rng.choice([1, 2, 3, 9, 18, 37, 74, 148]))))
+    joined = 0
+    for chunks, ctas in batches:
+        cs = np.concatenate([[0], np.cumsum(chunks)]).astype(np.int32)
+        rc = split(len(chunks), cs.ctypes.data_as(ctypes.POINTER(ctypes.c_int)), ctas, ctypes.byref(got))
+        assert rc == 0, (rc, chunks, ctas)
+        joined += got.value < min(4 * ctas, int(cs[-1]))
+    assert joined > 100                                                   # (some CTAs left one share for several warpgroups)
