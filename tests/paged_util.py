@@ -137,3 +137,34 @@ def check_rows(got, want, bound, dtype):
     err = np.abs(g - want)
     lim = bound * (1 + half) + half * np.abs(want) + torch.finfo(dtype).tiny
     assert (err <= lim).all(), (float((err / lim).max()), float(err.max()))
+
+
+def rows_and_bound(k, v, q):
+    """softmax(q . k / sqrt(128)) . v in 64 bits for q [heads][128], and a bound of an fp32 kernel's error,
+    element by element, for one KV head and at most 148 * 128 positions (a share of the kernels is then one chunk).
+
+    A softmax weight is off by a relative e, in the numerator and in the sum, so an output by at most 2 e of
+    the weighted mean of |v|. e is: the logit's error times ln 2, with A the sum of |q k| in log2 units: the
+    pair of a query 2^-22 of each product, fp32 sums of 24 products cut off at 2^-23, the products with the
+    norm and the scale, 2^-24 each of A: below 2^-18 A (high and low sums one after the other: 2^-17 A); the
+    pair of a share 2^-22; a chunk's 16 products cut off at 2^-23: 2^-19; 2^x and row sums of a chunk 2^-19;
+    the merge of at most 148 shares by 16 warps and of those 2^-18: together below 2^-17. Shares below fp16's
+    normal range are off by 2^-38 of the largest share, times a centroid below 5."""
+    z = (k @ q.T).T / math.sqrt(128.0)                                    # [heads][tokens]
+    p = np.exp(z - z.max(1, keepdims=True))
+    total = p.sum(1, keepdims=True)
+    A = (np.abs(k) @ np.abs(q.T)).T.max(1) / math.sqrt(128.0) * LOG2E
+    e = A * math.log(2) * 2.0 ** -17 + 2.0 ** -17
+    largest = (p * np.abs(v).max(1)).max(1, keepdims=True)
+    return p @ v / total, 2 * e[:, None] * (p @ np.abs(v)) / total + 5 * p.shape[1] * 2.0 ** -38 * largest / total
+
+
+def check_close(got, want, bound, dtype):
+    """got within the bound and half a step of its type of `want`."""
+    import torch
+    f = torch.finfo(dtype)
+    g = host_f32(got).astype(np.float64)
+    assert np.isfinite(g).all()
+    lim = bound * (1 + f.eps) + f.eps / 2 * np.abs(want) + f.tiny * f.eps
+    err = np.abs(g - want)
+    assert (err <= lim).all(), (float((err / lim).max()), float(err.max()))

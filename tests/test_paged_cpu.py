@@ -10,7 +10,7 @@ from oracle import blockgtq as bg
 from oracle import rope as orope
 from packed_cache_attention_b200 import kvq
 from tests import test_c_client as cc
-from tests.paged_util import angle_table, rotate_f32
+from tests.paged_util import angle_table, check_close, rotate_f32, rows_and_bound
 from tests.test_abi import L, WS_BYTES, _t4, buf  # noqa: F401
 
 ARG, SHAPE, DTYPE, RANGE, WORKSPACE, UNSUPPORTED = 1, 2, 3, 5, 6, 9
@@ -339,3 +339,34 @@ def test_decode_and_merge_agree_on_every_share(tmp_path):
         assert rc == 0, (rc, chunks, ctas)
         joined += got.value < min(4 * ctas, int(cs[-1]))
     assert joined > 100                                                   # (some CTAs left one share for several warpgroups)
+
+
+@pytest.mark.parametrize("scale", [1.0, 1e-4])
+@pytest.mark.parametrize("tokens", [5, 40, 300])
+def test_the_precision_bound_tells_a_share_of_11_bits_from_a_pair(tokens, scale):
+    """The kernels' shares restated: 2^(logit - M) |v| / sqrt(128) * 2^13 as an fp16 pair stays inside the bound of the GPU
+    tests, its high part alone does not, nor a fixed scale of 2 for small values. (The largest share of a row is a
+    power of two, so one token alone would not show.)"""
+    import torch
+    rng = np.random.default_rng(tokens)
+    code = kvq.kvq_codebook(4)[0].astype(np.float64)[rng.integers(0, 16, (tokens, 128))]
+    norm = (scale * 11.3 * np.exp(0.1 * rng.standard_normal(tokens))).astype(np.float16).astype(np.float32)
+    vn = norm * np.float32(1 / math.sqrt(128.0))
+    k, v, q = rng.standard_normal((tokens, 128)), code * vn[:, None].astype(np.float64), np.zeros((3, 128))
+    want, bound = rows_and_bound(k, v, q)
+
+    def rows(parts, M, s):
+        w = np.float32(2.0 ** -M)
+        y = (vn * np.float32(s)) * w
+        hi = y.astype(np.float16)
+        lo = (y - hi.astype(np.float32)).astype(np.float16)
+        share = hi.astype(np.float64) + (lo.astype(np.float64) if parts == 2 else 0.0)
+        out = (share @ code) / s / (w.astype(np.float64) * tokens)
+        return torch.from_numpy(np.repeat(out[None], 3, 0).astype(np.float32))
+    top = float(np.log2(vn).max())
+    check_close(rows(2, top, 8192.0), want, bound, torch.float32)
+    with pytest.raises(AssertionError):
+        check_close(rows(1, top, 8192.0), want, bound, torch.float32)
+    if scale < 1e-3:
+        with pytest.raises(AssertionError):
+            check_close(rows(2, 0.0, 2.0), want, bound, torch.float32)

@@ -1,15 +1,12 @@
 """Paged attention against rows in 64 bits where a fixed scale would lose digits: small and mixed value
-norms, values of zero, queries with one coordinate far above the rest.
-
-One KV head and at most 148 * 128 positions: a share (of a warpgroup, or a prefix split) is one chunk, so the
-bounds below count one chunk's roundings."""
+norms, values of zero, queries with one coordinate far above the rest."""
 import math
 
 import numpy as np
 import pytest
 
 from packed_cache_attention_b200 import kvq
-from tests.paged_util import LOG2E, Paged
+from tests.paged_util import Paged, check_close as check, rows_and_bound
 from tests.parity_util import host_f32
 
 pytestmark = pytest.mark.gpu
@@ -24,42 +21,17 @@ def dev():
     return torch.device("cuda:0")
 
 
-def exact_rows(P, q, lens, prefix, used=None):
-    """Rows in 64 bits and a bound of an fp32 kernel's error, element by element.
-
-    A softmax weight is off by a relative e, in the numerator and in the sum, so an output by at most 2 e of
-    the weighted mean of |v|. e is: the logit's error times ln 2, with A the sum of |q k| in log2 units: the
-    pair of a query 2^-22 of each product, fp32 sums of 24 products cut off at 2^-23, the products with the
-    norm and the scale, 2^-24 each of A: below 2^-18 A (high and low sums one after the other: 2^-17 A); the
-    pair of a share 2^-22; a chunk's 16 products cut off at 2^-23: 2^-19; 2^x and row sums of a chunk 2^-19;
-    the merge of at most 148 shares by 16 warps and of those 2^-18: together below 2^-17. Shares below fp16's
-    normal range are off by 2^-38 of the largest share, times a centroid below 5."""
+def exact_rows(P, q, lens, prefix):
+    """Rows in 64 bits of q [B][Hq][128] and the bound of an fp32 kernel's error (paged_util.rows_and_bound)."""
     q = host_f32(q).astype(np.float64)
-    B, Hq, _ = q.shape
     out, bound = np.zeros(q.shape), np.zeros(q.shape)
     pk, pv = P.kv(P.prefix_np, prefix)
     for b, n in enumerate(lens):
         k, v = P.kv(P.table_np[b], n)
         k, v = np.concatenate([pk, k], 1)[0], np.concatenate([pv, v], 1)[0]
-        z = (k @ q[b].T).T / math.sqrt(128.0)                             # [heads][tokens]
-        p = np.exp(z - z.max(1, keepdims=True))
-        total = p.sum(1, keepdims=True)
-        out[b] = p @ v / total
-        A = (np.abs(k) @ np.abs(q[b].T)).T.max(1) / math.sqrt(128.0) * LOG2E
-        e = A * math.log(2) * 2.0 ** -17 + 2.0 ** -17
-        largest = (p * np.abs(v).max(1)).max(1, keepdims=True)
-        bound[b] = 2 * e[:, None] * (p @ np.abs(v)) / total + 5 * p.shape[1] * 2.0 ** -38 * largest / total
+        if len(k):
+            out[b], bound[b] = rows_and_bound(k, v, q[b])
     return out, bound
-
-
-def check(got, want, bound, dtype):
-    import torch
-    f = torch.finfo(dtype)
-    g = host_f32(got).astype(np.float64)
-    assert np.isfinite(g).all()
-    lim = bound * (1 + f.eps) + f.eps / 2 * np.abs(want) + f.tiny * f.eps
-    err = np.abs(g - want)
-    assert (err <= lim).all(), (float((err / lim).max()), float(err.max()))
 
 
 def _pool(dev, seed, bits_k, bits_v, lens, prefix, scale_of):
@@ -94,6 +66,19 @@ def test_outputs_do_not_depend_on_the_scale_of_the_values(dev, bits_k, bits_v, h
             if dt == torch.float16 and scale == 1e3 and np.abs(want).max() > 6e4:
                 continue
             check(P.decode(q, lens, pre, out_dtype=dt), want, bound, dt)
+
+
+@pytest.mark.parametrize("scale", [1.0, 1e-4])
+@pytest.mark.parametrize("tokens", [1, 2, 5, 40])
+def test_few_tokens_of_equal_weight(dev, tokens, scale):
+    """A mean of few values, of own pages or of a prefix: shares of 11 bits would show."""
+    import torch
+    lens = [tokens] * 4
+    P, _ = _pool(dev, 100 + tokens, 3, 4, lens, tokens, lambda rng, n: np.full(n, scale))
+    q = torch.zeros((4, 8, 128), device=dev)
+    for own, pre in ((tokens, 0), (0, tokens), (tokens, tokens)):
+        want, bound = exact_rows(P, q, [own] * 4, pre)
+        check(P.decode(q, [own] * 4, pre), want, bound, torch.float32)
 
 
 @pytest.mark.parametrize("bits_k,bits_v,heads", [(3, 3, 8), (4, 8, 3), (8, 2, 4)])
