@@ -459,6 +459,91 @@ def test_a_refused_head_keeps_its_rows_and_no_others(dev, batch, head):
         assert torch.equal(again, want) and kvq.kvq_workspace_status(ws) == 0
 
 
+def test_the_largest_batch_behind_a_prefix(dev):
+    """1024 sequences of 8 heads: 64 groups of rows on the prefix, more CTAs than SMs."""
+    import torch
+    lens = ([0, 3, 140, 33] * 256)[:1024]
+    P = Paged(dev, 26, 3, 2, 3, 32, lens, prefix=300)
+    P.fill(lens, torch.bfloat16, prefix=300)
+    q = torch.randn((1024, 24, 128), device=dev)
+    got = P.decode(q, lens, 300)
+    rows = [0, 1, 15, 16, 17, 511, 514, 1022, 1023]
+    sub = Paged.__new__(Paged)
+    sub.__dict__.update(P.__dict__)
+    sub.table_np = P.table_np[rows]
+    check_rows(got[rows], *sub.attention(q[rows], [lens[b] for b in rows], 300), torch.float32)
+
+
+def test_the_largest_page(dev):
+    """Pages of 65536 positions, one of them entered by four tokens."""
+    import torch
+    lens = [65540, 7]
+    P = Paged(dev, 27, 1, 1, 2, 65536, lens, prefix=33)
+    P.fill(lens, torch.float16, prefix=33)
+    q = torch.randn((2, 2, 128), device=dev).half()
+    for prefix in (0, 33):
+        check_rows(P.decode(q, lens, prefix), *P.attention(q, lens, prefix), torch.float32)
+
+
+def test_one_query_and_one_sequence_for_many_rows(dev):
+    """Rows that share a query (stride 0), a sequence or its first pages as the prefix, and an output over the queries."""
+    import torch
+    P = Paged(dev, 28, 2, 3, 3, 64, [300, 128], prefix=0)
+    P.fill([300, 128], torch.bfloat16)
+    q = torch.randn((1, 8, 128), device=dev)
+    table = P.table[[0, 0, 1, 0, 1]].contiguous()
+    lens = [300, 120, 128, 300, 0]
+    call = lambda q, **kw: kvq.kvq_paged_decode_attn(q, P.pool, P.alloc, P.desc, table, P.ints(lens), **kw)  # noqa: E731
+    got = call(q.expand(5, 8, 128))
+    sub = Paged.__new__(Paged)
+    sub.__dict__.update(P.__dict__)
+    sub.table_np = P.table_np[[0, 0, 1, 0, 1]]
+    check_rows(got, *sub.attention(q.expand(5, 8, 128), lens), torch.float32)
+    assert torch.equal(got[0], got[3])
+    same = q.repeat(5, 1, 1)
+    assert call(same, out=same) is same and torch.equal(same, got)
+    lead = call(q.expand(5, 8, 128), prefix_pages=P.table[0, :2].contiguous(), prefix_len=100)
+    sub.prefix_np = P.table_np[0, :2]
+    check_rows(lead, *sub.attention(q.expand(5, 8, 128), lens, 100), torch.float32)
+    same = q.repeat(5, 1, 1)
+    call(same, prefix_pages=P.table[0, :2].contiguous(), prefix_len=100, out=same)
+    assert torch.equal(same, lead)
+
+
+def test_two_graphs_share_a_workspace(dev):
+    """Two captured decodes of different batches on one workspace, replayed in turn on one stream, with eager calls
+    between them."""
+    import torch
+    lens = [400, 0, 77, 129, 1, 300]
+    P = Paged(dev, 29, 1, 4, 4, 64, lens, prefix=260)
+    P.fill(lens, torch.bfloat16, prefix=260)
+    q = torch.randn((6, 8, 128), device=dev)
+    ws = kvq.kvq_paged_decode_workspace(P.desc, 6, 8, 260)
+    want = [P.decode(q, lens, 260), P.decode(q, lens)]
+    outs, n = [torch.empty_like(q) for _ in range(2)], P.ints(lens)
+    call = lambda i: kvq.kvq_paged_decode_attn(  # noqa: E731
+        q if i == 0 else q[:4], P.pool, P.alloc, P.desc, P.table if i == 0 else P.table[:4], n if i == 0 else n[:4],
+        prefix_pages=P.prefix_pages if i == 0 else None, prefix_len=260 if i == 0 else 0, ws=ws, out=outs[i] if i == 0 else outs[i][:4])
+    side = torch.cuda.Stream()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i, g in enumerate(graphs):
+        with torch.cuda.graph(g, stream=side):
+            call(i)
+    with torch.cuda.stream(side):
+        for r in range(30):
+            for o in outs:
+                o.fill_(float(r))
+            graphs[r % 2].replay()
+            if r % 3 == 0:
+                call((r + 1) % 2)
+            else:
+                graphs[(r + 1) % 2].replay()
+            side.synchronize()
+            assert torch.equal(outs[0], want[0]) and torch.equal(outs[1][:4], want[1][:4]) and bool((outs[1][4:] == r).all())
+    assert kvq.kvq_workspace_status(ws) == 0
+
+
 def test_calls_on_a_given_stream_without_buffers(dev):
     """Outputs and workspaces that a call makes belong to the stream it was given."""
     import torch
