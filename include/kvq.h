@@ -479,7 +479,8 @@ kvq_status kvq_paged_init(const void* alloc, const kvq_paged_desc* desc, void* p
  * K, V: [1][n_kv_heads][n_tokens][128] (one dtype; strides may differ).
  * The pages written must belong to one sequence each; calls on one pool may overlap on the GPU if
  * no page is written by one and used by another. cu_tokens: [batch + 1], device memory.
- * The call checks the pool's header on the device (KVQ_ERR_MISMATCH, nothing written) and every page
+ * The call checks the pool's header and the allocation's budget on the device (KVQ_ERR_MISMATCH in the
+ * header, no record written) and every page
  * index, length and position it uses: a sequence whose rows or positions do not fit (rows not ascending
  * or past n_tokens, more positions than max_pages hold, a page outside the pool) loses the tiles
  * concerned, a token whose position is outside the table is stored with a NaN norm, and the
@@ -504,8 +505,9 @@ size_t kvq_paged_decode_workspace_bytes(const kvq_paged_desc* desc, int batch, i
 /* Decode attention over a paged cache, one query token per sequence: query head hq of sequence
  * b attends with KV head hq / (n_q_heads / n_kv_heads) over the prefix (if any) and then the
  * sequence's own positions 0..seq_lens[b]-1, in one softmax; arithmetic and dequantization
- * as kvq_decode_attn. The prefix is dequantized once for the whole batch, not once per
- * sequence. A sequence with nothing to attend to gives a row of zeros.
+ * as kvq_decode_attn. The prefix is dequantized once per 128 query rows of a KV head
+ * (batch * n_q_heads / n_kv_heads rows), not once per sequence; for a few rows it costs as much
+ * as for 128. A sequence with nothing to attend to gives a row of zeros.
  * q: [batch][n_q_heads][1][128], rotated (kvq_rope); n_q_heads / n_kv_heads must be 1..8.
  * out: [batch][n_q_heads][128], contiguous, 16-byte aligned, of out_dtype (any kvq_dtype,
  * rounded once from fp32: the rows of a 16-bit type are the fp32 ones rounded).

@@ -20,8 +20,8 @@
 //
 // Order: the producers write Khat(j + 1) once S(j) is done and Vhat(j) once O(j - 1) is; S(j + 1) is
 // issued before O(j), into the other buffer, so it runs under the softmax of chunk j. A chunk takes
-// 5.3k cycles (K3V3, 128 rows); with tokens as lanes, whose row maxima need a warp reduction per
-// row, it took 12.9k.
+// 5.6k cycles (3.2 us; K3V3, 128 rows), 0.3k of them for the low parts of P' and the values' part of M;
+// with tokens as lanes, whose row maxima need a warp reduction per row, it took 12.9k.
 //
 // Every wait is bounded, as in kvq_decode_gtq; a CTA that gave up, or met a bad header or page,
 // leaves NaN maxima, at which the merge leaves the rows as they are.
@@ -183,8 +183,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kvq_prefix_gtq(const PrefixArg
   } else if (is_issuer) {
     // ------------------------------------------------------------------ issuing warp
     // One lane issues the products. Elected for the logits, which the consumers wait for (2.96 -> 2.79 us
-    // a chunk), lane 0 for O's: those issued as fast held up the warps' own tensor memory accesses
-    // (3.2 us). Lanes 0..3 each copy one tile of a chunk.
+    // a chunk, with high parts of P' alone), lane 0 for O's: those issued as fast held up the warps' own
+    // tensor memory accesses (3.2 us). Lanes 0..3 each copy one tile of a chunk.
     int nk = 0, nv = 0;                                     // chunks whose K (V) copies are started
     Ring rk, rv;
     auto copy_part = [&](int& i, Ring& r, uint64_t* bars, int skip, int bytes, int at) {
