@@ -260,7 +260,7 @@ __device__ __forceinline__ void store_f32(void* p, int dtype, int64_t i, float v
 // absolute error: 2^-36 where low parts have rows of their own in the product and are stored times
 // 2^11 (decode), 2^-25 where they join the high parts' sums (prefix); that is 2^-45 and 2^-38 of the
 // row's largest share. (M of the logits alone and a fixed scale lost the shares of small values:
-// outputs off by 7e-4 at |v| = 1e-3 and 0.1 at 1e-5. The maxima of the prefix move sooner, which a chunk's
+// over 4096 tokens of a prefix 2e-3 of the output at |v| = 1e-3, 0.2 at 1e-5. The maxima of the prefix move sooner, which a chunk's
 // time does not show; for decode the same costs 3 %.)
 constexpr int kPgThr = 6, kPreThr = 2;
 constexpr float kPgScale = 512.0f, kPreScale = 8192.0f, kPgLow = 2048.0f;
